@@ -205,6 +205,117 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
              float* dWo, float* dbo, void* stream);
 
 /*
+ * glu_fwd, glu_bwd_input, glu_bwd_weights - the gated feed-forward block, the MLP
+ * block with a gate (the pages' MLP has none; Shazeer, "GLU Variants Improve
+ * Transformer", 2020).  It is split over slices like the MLP block, [Ag | Au] by
+ * columns and B by rows (STRONGHOLD slides, items 7-8); all t slices run in every call.
+ *   forward   G = X Ag + ag,  U = X Au + au,  Y = act(G) * U
+ *             O = R + dropout(Y B + b)               (the MLP block's dropout mask)
+ *   backward  dZ = dO m / (1-p);  dY = dZ B^T;  dG = dY U act'(G);  dU = dY act(G)
+ *             dX = [dO +] dG Ag^T + dU Au^T
+ *             dA (+)= X^T [dG | dU],  da (+)= sum_tok [dG | dU],  dB (+)= Y^T dZ,  db (+)= sum_tok dZ
+ * act is GLU_SILU, act(x) = x / (1 + exp(-x)), or GLU_GELU, the MLP block's tanh form.
+ *
+ *   A [h, 2 ffn] = [Ag | Au], a [2 ffn], GU [tokens, 2 ffn] = [G | U], dGU likewise,
+ *   dA [h, 2 ffn], da [2 ffn]; the other shapes, types and constraints as for mlp_fwd
+ *   (t must divide ffn, and ffn / t and h be multiples of 8; ffn <= 2^29).
+ *
+ * glu_fwd: a and b may be NULL (no bias), R NULL means R = X.  GU [tokens, 2 ffn] is
+ *   written for the backward and may be NULL; Y [tokens, ffn] is always written.
+ *   Y is formed from the fp32 G and U, before their rounding to bf16.
+ * glu_bwd_input: the part of the backward that the block before waits for.  GU as
+ *   glu_fwd wrote it.  Writes dGU, dX, and dZ where p > 0; without dropout dZ is dO
+ *   and dZ may be NULL.  residual_grad as for mlp_bwd.
+ * glu_bwd_weights: the part that only the update waits for, so that a pipeline stage
+ *   may send dX on first.  dZ is glu_bwd_input's, or dO where p = 0.  accumulate as
+ *   for mlp_bwd.  da and db may be NULL.  scratch: [tokens, h] fp32, or NULL; holds
+ *   the transposed copies of mlp_set_wgrad_transpose where the products are large.
+ *
+ * Outputs may not overlap inputs.  These calls use none of the library's static device
+ * memory but the status word: the same call gives the same bits on every stream, and
+ * graphs that were captured on one stream may run at once on others.
+ * Each returns MLP_OK or an error code.
+ */
+enum { GLU_SILU = 0, GLU_GELU = 1 };
+
+int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
+            const mlp_bf16* X, const mlp_bf16* A, const mlp_bf16* a, const mlp_bf16* B, const mlp_bf16* b,
+            const mlp_bf16* R, mlp_bf16* GU, mlp_bf16* Y, mlp_bf16* O, void* stream);
+int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
+                  int residual_grad, const mlp_bf16* dO, const mlp_bf16* A, const mlp_bf16* B, const mlp_bf16* GU,
+                  mlp_bf16* dZ, mlp_bf16* dGU, mlp_bf16* dX, void* stream);
+int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const mlp_bf16* X, const mlp_bf16* dZ,
+                    const mlp_bf16* Y, const mlp_bf16* dGU, float* dA, float* da, float* dB, float* db, float* scratch,
+                    void* stream);
+
+/*
+ * qk_norm_rope_fwd, qk_norm_rope_bwd - norms of queries and keys for each head and
+ * the rotation by their positions, in one pass (Zhang & Sennrich 2019 for the norm,
+ * Su et al. 2021 for the rotation; the pages' model has neither).  For a head vector x
+ * of d elements of a token:
+ *   n = x * (mean(x^2) + eps)^(-1/2) * w          (w = wq or wk; n = x where both are NULL)
+ *   each pair (n_i, n_j) of the first rot elements turns by the angle
+ *   pos[axis(i)][token] * inv_freq[i]:  (n_i cos - n_j sin, n_j cos + n_i sin)
+ *   pair i < rot/2 is (i, i + rot/2), or (2i, 2i + 1) where interleaved = 1; the
+ *   elements from rot on are not turned.
+ * Axes: n_axes (1 to 3) rows of positions (e.g. time, height, width).  The first s0
+ * pairs turn with axis 0, the next s1 with axis 1, the next s2 with axis 2;
+ * s0 + s1 + s2 = rot / 2, and sections of axes that are not there are 0.
+ *   tokens in [1, 2^31), nq, nk >= 1 heads of queries and keys; d a multiple of 8, at
+ *   most 256; rot a multiple of 8, 8 <= rot <= d; eps >= 0.
+ *   wq, wk [d] bf16 or both NULL; pos [n_axes, tokens] int32 (any value, negative ones
+ *   too); inv_freq [rot/2] fp32, radians per position.
+ *   Q, K, Qo, Ko, and in the backward dQo, dKo (gradients of Qo, Ko), dQ, dK:
+ *   [tokens, heads, d] bf16, 16-byte aligned, a token's heads side by side, rows ld
+ *   elements apart (a multiple of 8, at least heads * d): the queries and keys inside a
+ *   fused projection's output, for instance.  An output may be the same memory as an
+ *   input (same pointer and ld); otherwise they may not overlap.
+ * Angles are exact to 2^-30 of a turn for positions up to 2^22, and to 2^-21 of a
+ * turn for any.
+ * Backward: dwq, dwk [d] fp32 are added to (accumulate = 1) or overwritten (0); ws is
+ * an fp32 workspace of QK_NORM_ROPE_WS_ROWS * 2 * d floats.  Without the norm (wq and
+ * wk NULL) Q, K, dwq, dwk and ws are not used and may be NULL.  Deterministic.
+ * Returns MLP_OK or an error code (nothing enqueued unless MLP_ECUDA).
+ */
+#define QK_NORM_ROPE_WS_ROWS 1024
+
+int qk_norm_rope_fwd(int64_t tokens, int nq, int nk, int d, int rot, int interleaved, int n_axes, int s0, int s1, int s2,
+                     float eps, const mlp_bf16* wq, const mlp_bf16* wk, const int32_t* pos, const float* inv_freq,
+                     const mlp_bf16* Q, int64_t ldq, const mlp_bf16* K, int64_t ldk, mlp_bf16* Qo, int64_t ldqo,
+                     mlp_bf16* Ko, int64_t ldko, void* stream);
+int qk_norm_rope_bwd(int64_t tokens, int nq, int nk, int d, int rot, int interleaved, int n_axes, int s0, int s1, int s2,
+                     float eps, const mlp_bf16* wq, const mlp_bf16* wk, const int32_t* pos, const float* inv_freq,
+                     int accumulate, const mlp_bf16* Q, int64_t ldq, const mlp_bf16* K, int64_t ldk,
+                     const mlp_bf16* dQo, int64_t lddqo, const mlp_bf16* dKo, int64_t lddko, mlp_bf16* dQ, int64_t lddq,
+                     mlp_bf16* dK, int64_t lddk, float* dwq, float* dwk, float* ws, void* stream);
+
+/*
+ * attn_rope_fwd, attn_rope_bwd - the attention block with head norms and rotation of
+ * its queries and keys (qk_norm_rope_fwd / _bwd with nq = nk = nh) between the QKV
+ * projection and the attention core:
+ *   forward   QKV = X Wqkv + bqkv;  [Qr | Kr] = norm and rotation of its queries and
+ *             keys;  P = softmax(mask(Qr Kr^T / sqrt(d)));  the rest as attn_fwd
+ *   backward  as attn_bwd on Qr, Kr; then dQKV's queries and keys, and dwq, dwk
+ * QKr [tokens, 2h] bf16 holds [Qr | Kr] (written by the forward, read by the backward);
+ * QKV holds the projection itself.  dwq, dwk and ws as for qk_norm_rope_bwd.  The other
+ * arguments are those of attn_fwd / attn_bwd and qk_norm_rope_fwd.
+ * Returns MLP_OK or an error code.
+ */
+int attn_rope_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+                  int rot, int interleaved, int n_axes, int s0, int s1, int s2, float eps, const mlp_bf16* wq,
+                  const mlp_bf16* wk, const int32_t* pos, const float* inv_freq, const mlp_bf16* X,
+                  const mlp_bf16* Wqkv, const mlp_bf16* bqkv, const mlp_bf16* Wo, const mlp_bf16* bo,
+                  const mlp_bf16* R, mlp_bf16* QKV, mlp_bf16* QKr, float* S, mlp_bf16* P, mlp_bf16* O, mlp_bf16* out,
+                  void* stream);
+int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+                  int rot, int interleaved, int n_axes, int s0, int s1, int s2, float eps, const mlp_bf16* wq,
+                  const mlp_bf16* wk, const int32_t* pos, const float* inv_freq, int residual_grad, int accumulate,
+                  const mlp_bf16* dOut, const mlp_bf16* X, const mlp_bf16* Wqkv, const mlp_bf16* Wo,
+                  const mlp_bf16* QKV, const mlp_bf16* QKr, const mlp_bf16* P, const mlp_bf16* O, mlp_bf16* dZ,
+                  mlp_bf16* dO, float* dP, mlp_bf16* dS, mlp_bf16* dQKV, mlp_bf16* dX, float* dWqkv, float* dbqkv,
+                  float* dWo, float* dbo, float* dwq, float* dwk, float* ws, void* stream);
+
+/*
  * mlp_sync_status - synchronise `stream`, then return and clear the device status
  * word: MLP_OK, or MLP_ETIMEOUT if a kernel gave up on a bounded wait since the
  * last call (mlp_last_error() then names the wait), or MLP_ECUDA.
@@ -338,7 +449,9 @@ int mlp_trace_begin(int capacity);
  * B4, B5 of the forward/backward; 10 = dropout backward + db; 11 = column sum
  * for da; 12 = accumulator reset; 14 = adam_step; 15 = the transposed copies of
  * X and dZ (mlp_set_wgrad_transpose); 20 = attention GEMMs; 21 =
- * softmax forward / backward; 22 = fused attention core), mnk[3i..3i+2] = the
+ * softmax forward / backward; 22 = fused attention core; 30..34 = the gated block's
+ * GEMMs G and U with the gate, O, dY with the gate's gradient, dX, dA and dB; 40, 41 =
+ * head norms and rotation, forward and backward; 42 = their weight gradients), mnk[3i..3i+2] = the
  * launch's M, N, K (GEMMs; for the fused core: query rows, keys per sequence, d)
  * or rows, columns, 0, and ms[i] = its device time in milliseconds.  Any output
  * pointer may be NULL.  Returns the number of entries written, or an error code.

@@ -50,6 +50,40 @@ __device__ __forceinline__ float gelu_prime_f(float x) {
   return fmaf(2.0f * x * ds, (e * r) * r, r);
 }
 
+// ---- gates of the gated feed-forward block: act(x) and its derivative, a NaN staying a NaN
+enum GluAct : int { kActSilu = 0, kActGelu = 1 };
+
+// x * sig(x), sig(x) = r = 1 / (1 + e), e = exp(-x): below x = -80 the value is under
+// 2e-33 in magnitude, and e is held at exp(80) there so that it stays finite.
+// derivative: r + x r (1 - r), with 1 - r = e r.
+__device__ __forceinline__ void silu_both_f(float x, float& v, float& dv) {
+  const float e = __expf(fminf(-x, 80.0f));
+  const float r = rcp_approx(1.0f + e);
+  const float xr = fmaxf(x, -80.0f) * r;
+  v = x == x ? xr : x;
+  dv = x == x ? fmaf(e * r, fminf(xr, 80.0f), r) : x;
+}
+__device__ __forceinline__ float silu_f(float x) {
+  const float v = fmaxf(x, -80.0f) * rcp_approx(1.0f + __expf(fminf(-x, 80.0f)));
+  return x == x ? v : x;
+}
+__device__ __forceinline__ float gelu_gate_f(float x) {
+  const float v = gelu_f(x);
+  return x == x ? v : x;
+}
+// gelu_f and gelu_prime_f sharing their exponential.
+__device__ __forceinline__ void gelu_both_f(float x, float& v, float& dv) {
+  const float xn = fmaxf(x, -30.0f);
+  const float xc = fminf(xn, 30.0f);
+  const float x2 = xc * xc;
+  const float s = kSqrt2OverPi * fmaf(kGeluCubic * xc, x2, xc);
+  const float ds = kSqrt2OverPi * fmaf(3.0f * kGeluCubic, x2, 1.0f);
+  const float e = __expf(fminf(-2.0f * s, 80.0f));
+  const float r = rcp_approx(1.0f + e);
+  v = x == x ? xn * r : x;
+  dv = x == x ? fmaf(2.0f * xc * ds, (e * r) * r, r) : x;
+}
+
 __device__ __forceinline__ uint64_t splitmix64_at(uint64_t seed, uint64_t e) {
   uint64_t z = seed + (e + 1ull) * 0x9E3779B97F4A7C15ull;
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;

@@ -31,6 +31,7 @@
 #include "elementwise.cuh"
 #include "gb_mlp.h"
 #include "gemm_tc.cuh"
+#include "qk_rope.cuh"
 
 using namespace gbmlp;
 
@@ -71,7 +72,9 @@ TraceState g_trace;
 enum TraceKind {
   kTraceF1 = 0, kTraceF2 = 1, kTraceB2 = 2, kTraceB3 = 3, kTraceB4 = 4, kTraceB5 = 5,
   kTraceDropBwd = 10, kTraceColsum = 11, kTraceZero = 12, kTraceOther = 13, kTraceAdam = 14, kTraceTranspose = 15,
-  kTraceAttnGemm = 20, kTraceSoftmax = 21, kTraceAttnCore = 22
+  kTraceAttnGemm = 20, kTraceSoftmax = 21, kTraceAttnCore = 22,
+  kTraceGlu = 30, kTraceGluOut = 31, kTraceDGlu = 32, kTraceGluDX = 33, kTraceGluDW = 34,
+  kTraceQkRope = 40, kTraceQkRopeBwd = 41, kTraceQkDw = 42
 };
 
 // Records the start event of the next launch; returns its slot or -1.
@@ -111,10 +114,10 @@ struct DeviceState {
   int* sched_ctr = nullptr;    // tile counters of the dynamic scheduler, 2 per region
   cudaStream_t split_owner[kSplitRegions] = {};  // the stream each region belongs to
   int split_regions_used = 0;
-  bool gemm_attr[32] = {};  // per GEMM instantiation: dynamic smem attribute set
+  bool gemm_attr[96] = {};  // per GEMM instantiation: dynamic smem attribute set
   bool fa_attr = false;     // fused attention core: dynamic smem attribute set
   bool fb_attr = false;     // fused attention backward core: dynamic smem attribute set
-  int max_pairs[32] = {};   // per CTA-pair instantiation: co-resident clusters of two
+  int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
 
 
@@ -325,6 +328,8 @@ int launch_transposes(cudaStream_t s, int64_t rows, int cols, TransposeJob j0, T
   trace_post(ts, s, kTraceTranspose, rows, cols, 0);
   return launch_check(e, what);
 }
+
+#include "qk_rope_host.cuh"
 
 template <int CHUNKS>
 cudaError_t softmax_warp_launch(DeviceState* st, const float* S, uint16_t* P, int64_t rows, int cols, cudaStream_t s) {
@@ -549,10 +554,18 @@ int check_attn_shape(int h, int nh, int t, int64_t tokens, int seq_len, float p)
 // in HBM (a batched GEMM, the row softmax, a batched GEMM).
 std::atomic<int> g_attn_fused{1};
 
+// Where the attention core reads its queries and keys: rows `ld` elements apart, in
+// QKV (ld = 3h), or after head norms and rotation in a buffer of their own.
+struct QkSource {
+  const uint16_t* q;
+  const uint16_t* k;
+  int64_t ld;
+};
+
 // The fused attention core over every (sequence, head, query tile); P and O as in
 // attn_fwd.  Returns MLP_OK or an error code.
-int attn_core_fused(DeviceState* st, const uint16_t* QKV, uint16_t* P, uint16_t* O, int h, int nh, int L, int ns,
-                    cudaStream_t s) {
+int attn_core_fused(DeviceState* st, const QkSource& qk, const uint16_t* QKV, uint16_t* P, uint16_t* O, int h, int nh,
+                    int L, int ns, cudaStream_t s) {
   const int d = h / nh;
   const int64_t h3 = 3 * (int64_t)h;
   FaParams fp;
@@ -566,10 +579,10 @@ int attn_core_fused(DeviceState* st, const uint16_t* QKV, uint16_t* P, uint16_t*
   fp.P = P;
   CUtensorMap mQ, mK, mV, mP, mO;
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  int rc = make_map4(&mQ, bf, 2, QKV, d, L, h3, nh, d, ns, L * h3, 64, kFaTile, CU_TENSOR_MAP_SWIZZLE_128B,
+  int rc = make_map4(&mQ, bf, 2, qk.q, d, L, qk.ld, nh, d, ns, L * qk.ld, 64, kFaTile, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (!rc)
-    rc = make_map4(&mK, bf, 2, QKV + h, d, L, h3, nh, d, ns, L * h3, 64, kFaTile, CU_TENSOR_MAP_SWIZZLE_128B,
+    rc = make_map4(&mK, bf, 2, qk.k, d, L, qk.ld, nh, d, ns, L * qk.ld, 64, kFaTile, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (!rc)
     rc = make_map4(&mV, bf, 2, QKV + 2 * h, d, L, h3, nh, d, ns, L * h3, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -598,7 +611,7 @@ int attn_core_fused(DeviceState* st, const uint16_t* QKV, uint16_t* P, uint16_t*
 
 // The fused attention core of the backward: dK and dV into dQKV, dS (P's shape)
 // into dS; delta = rowsum(dO * O) must be in `delta`.
-int attn_core_bwd_fused(DeviceState* st, const uint16_t* QKV, const uint16_t* P, const uint16_t* dO,
+int attn_core_bwd_fused(DeviceState* st, const QkSource& qk, const uint16_t* QKV, const uint16_t* P, const uint16_t* dO,
                         const float* delta, uint16_t* dS, uint16_t* dQKV, int h, int nh, int L, int ns,
                         cudaStream_t s) {
   const int d = h / nh;
@@ -617,7 +630,7 @@ int attn_core_bwd_fused(DeviceState* st, const uint16_t* QKV, const uint16_t* P,
   const auto sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
   const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   int rc = make_map4(&mV, bf, 2, QKV + 2 * h, d, L, h3, nh, d, ns, L * h3, 64, kFaTile, sw128, l2);
-  if (!rc) rc = make_map4(&mQ, bf, 2, QKV, d, L, h3, nh, d, ns, L * h3, 64, kFaTile, sw128, l2);
+  if (!rc) rc = make_map4(&mQ, bf, 2, qk.q, d, L, qk.ld, nh, d, ns, L * qk.ld, 64, kFaTile, sw128, l2);
   if (!rc) rc = make_map4(&mdO, bf, 2, dO, d, L, h, nh, d, ns, (int64_t)L * h, 64, kFaTile, sw128, l2);
   if (!rc) rc = make_map4(&mP, bf, 2, P, L, L, L, nh, LL, ns, nh * LL, 64, kFaTile, sw128, l2);
   if (!rc)
@@ -709,14 +722,23 @@ int adam_step(int64_t n, const float* grad, float grad_scale, float* master, flo
   return launch_check(e, "adam_step");
 }
 
-int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
-             const mlp_bf16* X, const mlp_bf16* Wqkv, const mlp_bf16* bqkv, const mlp_bf16* Wo, const mlp_bf16* bo,
-             const mlp_bf16* R, mlp_bf16* QKV, float* S, mlp_bf16* P, mlp_bf16* O, mlp_bf16* out, void* stream) {
+// rope: null for attn_fwd; attn_rope_fwd's norms and rotation of the queries and keys,
+// which go to QKr [tokens, 2h] and are read by the core from there.
+static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr, int h, int nh, int t, int64_t tokens,
+                         int seq_len, float p, uint64_t seed, uint64_t token_offset, const mlp_bf16* X,
+                         const mlp_bf16* Wqkv, const mlp_bf16* bqkv, const mlp_bf16* Wo, const mlp_bf16* bo,
+                         const mlp_bf16* R, mlp_bf16* QKV, float* S, mlp_bf16* P, mlp_bf16* O, mlp_bf16* out,
+                         void* stream) {
   int rc = check_attn_shape(h, nh, t, tokens, seq_len, p);
   if (rc) return rc;
-  rc = check_ptrs("attn_fwd", {X, Wqkv, bqkv, Wo, bo, QKV, S, P, O, out});
+  rc = check_ptrs(what, {X, Wqkv, bqkv, Wo, bo, QKV, S, P, O, out});
   if (rc) return rc;
-  if (R != nullptr && !aligned16(R)) return fail(MLP_EALIGN, "attn_fwd: R is not 16-byte aligned");
+  if (R != nullptr && !aligned16(R)) return fail(MLP_EALIGN, "%s: R is not 16-byte aligned", what);
+  if (rope != nullptr) {
+    rc = check_qk_rope(what, tokens, nh, nh, h / nh, *rope);
+    if (!rc) rc = check_qk_rows(what, "QKr", QKr, 2 * (int64_t)h, 2 * nh, h / nh);
+    if (rc) return rc;
+  }
   DeviceState* st = nullptr;
   rc = device_state(&st);
   if (rc) return rc;
@@ -732,9 +754,23 @@ int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   e.bias = bqkv;
   rc = gemm(st, X, false, h, Wqkv, true, h3, T, (int)h3, h, e, s, kTraceAttnGemm);
   if (rc) return rc;
+  QkSource qk{QKV, QKV + h, h3};
+  if (rope != nullptr) {
+    QkRopeParams rp{};
+    fill_qk_rope(&rp, tokens, nh, nh, d, *rope);
+    rp.q = QKV;
+    rp.k = QKV + h;
+    rp.ldq = rp.ldk = h3;
+    rp.oq = QKr;
+    rp.ok = QKr + h;
+    rp.ldoq = rp.ldok = 2 * (int64_t)h;
+    rc = launch_qk_rope(st, rp, rope->interleaved, s);
+    if (rc) return rc;
+    qk = QkSource{QKr, QKr + h, 2 * (int64_t)h};
+  }
   if (g_attn_fused.load(std::memory_order_relaxed) && ((d + 15) & ~15) <= kFaMaxAtoms * 64) {
     // S = Q K^T / sqrt(d), P = softmax(S), O = P V in one kernel; S stays on chip
-    rc = attn_core_fused(st, QKV, P, O, h, nh, L, ns, s);
+    rc = attn_core_fused(st, qk, QKV, P, O, h, nh, L, ns, s);
     if (rc) return rc;
     EpiParams ezf{};
     ezf.kind = kEpiDropRes;
@@ -749,7 +785,7 @@ int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   EpiParams es{};
   es.kind = kEpiScaleMask;
   es.alpha = 1.0f / std::sqrt((float)d);
-  rc = gemm_batched(st, {QKV, false, L, d, h3, d, L * h3}, {QKV + h, false, L, d, h3, d, L * h3},
+  rc = gemm_batched(st, {qk.q, false, L, d, qk.ld, d, L * qk.ld}, {qk.k, false, L, d, qk.ld, d, L * qk.ld},
                     {S, L, L, L, LL, nh * LL}, L, L, d, nh, ns, es, s, kTraceAttnGemm, kCausalSkipUpper);
   if (rc) return rc;
   rc = softmax_launch(st, S, P, (int64_t)ns * nh * L, L, s);
@@ -771,15 +807,43 @@ int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   return gemm(st, O, false, h, Wo, true, h, T, h, h, ez, s, kTraceAttnGemm);
 }
 
-int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
-             int residual_grad, int accumulate, const mlp_bf16* dOut, const mlp_bf16* X, const mlp_bf16* Wqkv,
-             const mlp_bf16* Wo, const mlp_bf16* QKV, const mlp_bf16* P, const mlp_bf16* O, mlp_bf16* dZ,
-             mlp_bf16* dO, float* dP, mlp_bf16* dS, mlp_bf16* dQKV, mlp_bf16* dX, float* dWqkv, float* dbqkv,
-             float* dWo, float* dbo, void* stream) {
+int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+             const mlp_bf16* X, const mlp_bf16* Wqkv, const mlp_bf16* bqkv, const mlp_bf16* Wo, const mlp_bf16* bo,
+             const mlp_bf16* R, mlp_bf16* QKV, float* S, mlp_bf16* P, mlp_bf16* O, mlp_bf16* out, void* stream) {
+  return attn_fwd_impl("attn_fwd", nullptr, nullptr, h, nh, t, tokens, seq_len, p, seed, token_offset, X, Wqkv, bqkv, Wo,
+                       bo, R, QKV, S, P, O, out, stream);
+}
+
+int attn_rope_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+                  int rot, int interleaved, int n_axes, int s0, int s1, int s2, float eps, const mlp_bf16* wq,
+                  const mlp_bf16* wk, const int32_t* pos, const float* inv_freq, const mlp_bf16* X,
+                  const mlp_bf16* Wqkv, const mlp_bf16* bqkv, const mlp_bf16* Wo, const mlp_bf16* bo,
+                  const mlp_bf16* R, mlp_bf16* QKV, mlp_bf16* QKr, float* S, mlp_bf16* P, mlp_bf16* O, mlp_bf16* out,
+                  void* stream) {
+  const QkRopeArgs rope{rot, interleaved, n_axes, s0, s1, s2, eps, wq, wk, pos, inv_freq};
+  return attn_fwd_impl("attn_rope_fwd", &rope, QKr, h, nh, t, tokens, seq_len, p, seed, token_offset, X, Wqkv, bqkv, Wo,
+                       bo, R, QKV, S, P, O, out, stream);
+}
+
+// rope: null for attn_bwd; with it the core reads the queries and keys from QKr, and
+// its gradients for them, left in dQKV, become those of the projection there.
+static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf16* QKr, float* dwq, float* dwk,
+                         float* ws, int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed,
+                         uint64_t token_offset, int residual_grad, int accumulate, const mlp_bf16* dOut,
+                         const mlp_bf16* X, const mlp_bf16* Wqkv, const mlp_bf16* Wo, const mlp_bf16* QKV,
+                         const mlp_bf16* P, const mlp_bf16* O, mlp_bf16* dZ, mlp_bf16* dO, float* dP, mlp_bf16* dS,
+                         mlp_bf16* dQKV, mlp_bf16* dX, float* dWqkv, float* dbqkv, float* dWo, float* dbo,
+                         void* stream) {
   int rc = check_attn_shape(h, nh, t, tokens, seq_len, p);
   if (rc) return rc;
-  rc = check_ptrs("attn_bwd", {dOut, X, Wqkv, Wo, QKV, P, O, dZ, dO, dP, dS, dQKV, dX, dWqkv, dbqkv, dWo, dbo});
+  rc = check_ptrs(what, {dOut, X, Wqkv, Wo, QKV, P, O, dZ, dO, dP, dS, dQKV, dX, dWqkv, dbqkv, dWo, dbo});
   if (rc) return rc;
+  if (rope != nullptr) {
+    rc = check_qk_rope(what, tokens, nh, nh, h / nh, *rope);
+    if (!rc) rc = check_qk_rows(what, "QKr", QKr, 2 * (int64_t)h, 2 * nh, h / nh);
+    if (!rc && rope->wq != nullptr) rc = check_ptrs("norm weight gradients and their workspace", {dwq, dwk, ws});
+    if (rc) return rc;
+  }
   DeviceState* st = nullptr;
   rc = device_state(&st);
   if (rc) return rc;
@@ -787,6 +851,7 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   const int T = (int)tokens, d = h / nh, L = seq_len, ns = T / L;
   const int64_t h3 = 3 * (int64_t)h, LL = (int64_t)L * L;
   const int acc = accumulate ? 1 : 0;
+  const QkSource qk = rope != nullptr ? QkSource{QKr, QKr + h, 2 * (int64_t)h} : QkSource{QKV, QKV + h, h3};
   // dZ = dropout'(dOut), dbo (+)= sum dZ
   {
     const DropoutParams drop = make_dropout(p, seed, token_offset, h);
@@ -839,9 +904,9 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
       rc = launch_check(e, "softmax-gradient row sums");
       if (rc) return rc;
     }
-    rc = attn_core_bwd_fused(st, QKV, P, dO, delta, dS, dQKV, h, nh, L, ns, s);
+    rc = attn_core_bwd_fused(st, qk, QKV, P, dO, delta, dS, dQKV, h, nh, L, ns, s);
     if (rc) return rc;
-    rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {QKV + h, true, d, L, h3, d, L * h3},
+    rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {qk.k, true, d, L, qk.ld, d, L * qk.ld},
                       {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo);
     if (rc) return rc;
   } else {
@@ -871,12 +936,25 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   rc = gemm_batched(st, {dO, false, L, d, h, d, (int64_t)L * h}, {QKV + 2 * h, false, L, d, h3, d, L * h3},
                     {dS, L, L, L, LL, nh * LL}, L, L, d, nh, ns, eg, s, kTraceAttnGemm, kCausalSkipUpper);
   if (rc) return rc;
-  rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {QKV + h, true, d, L, h3, d, L * h3},
+  rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {qk.k, true, d, L, qk.ld, d, L * qk.ld},
                     {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo);
   if (rc) return rc;
-  rc = gemm_batched(st, {dS, true, L, L, L, LL, nh * LL}, {QKV, true, d, L, h3, d, L * h3},
+  rc = gemm_batched(st, {dS, true, L, L, L, LL, nh * LL}, {qk.q, true, d, L, qk.ld, d, L * qk.ld},
                     {dQKV + h, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKFrom);
   if (rc) return rc;
+  }
+  if (rope != nullptr) {
+    // the core's dQ and dK are those of the turned, normed vectors: in place, to the projection's
+    QkRopeParams rp{};
+    fill_qk_rope(&rp, tokens, nh, nh, d, *rope);
+    rp.q = QKV;
+    rp.k = QKV + h;
+    rp.gq = rp.oq = dQKV;
+    rp.gk = rp.ok = dQKV + h;
+    rp.ldq = rp.ldk = rp.ldgq = rp.ldgk = rp.ldoq = rp.ldok = h3;
+    rp.ws = ws;
+    rc = launch_qk_rope_bwd(st, rp, rope->interleaved, dwq, dwk, acc, s);
+    if (rc) return rc;
   }
   // dbqkv (+)= sum dQKV; dWqkv (+)= X^T dQKV; dX = [dOut +] dQKV Wqkv^T
   {
@@ -910,6 +988,235 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
   ex.in0 = residual_grad ? dOut : nullptr;
   ex.out0 = dX;
   return gemm(st, dQKV, false, h3, Wqkv, false, h3, T, h, (int)h3, ex, s, kTraceAttnGemm);
+}
+
+int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+             int residual_grad, int accumulate, const mlp_bf16* dOut, const mlp_bf16* X, const mlp_bf16* Wqkv,
+             const mlp_bf16* Wo, const mlp_bf16* QKV, const mlp_bf16* P, const mlp_bf16* O, mlp_bf16* dZ,
+             mlp_bf16* dO, float* dP, mlp_bf16* dS, mlp_bf16* dQKV, mlp_bf16* dX, float* dWqkv, float* dbqkv,
+             float* dWo, float* dbo, void* stream) {
+  return attn_bwd_impl("attn_bwd", nullptr, nullptr, nullptr, nullptr, nullptr, h, nh, t, tokens, seq_len, p, seed,
+                       token_offset, residual_grad, accumulate, dOut, X, Wqkv, Wo, QKV, P, O, dZ, dO, dP, dS, dQKV, dX,
+                       dWqkv, dbqkv, dWo, dbo, stream);
+}
+
+int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
+                  int rot, int interleaved, int n_axes, int s0, int s1, int s2, float eps, const mlp_bf16* wq,
+                  const mlp_bf16* wk, const int32_t* pos, const float* inv_freq, int residual_grad, int accumulate,
+                  const mlp_bf16* dOut, const mlp_bf16* X, const mlp_bf16* Wqkv, const mlp_bf16* Wo,
+                  const mlp_bf16* QKV, const mlp_bf16* QKr, const mlp_bf16* P, const mlp_bf16* O, mlp_bf16* dZ,
+                  mlp_bf16* dO, float* dP, mlp_bf16* dS, mlp_bf16* dQKV, mlp_bf16* dX, float* dWqkv, float* dbqkv,
+                  float* dWo, float* dbo, float* dwq, float* dwk, float* ws, void* stream) {
+  const QkRopeArgs rope{rot, interleaved, n_axes, s0, s1, s2, eps, wq, wk, pos, inv_freq};
+  return attn_bwd_impl("attn_rope_bwd", &rope, QKr, dwq, dwk, ws, h, nh, t, tokens, seq_len, p, seed, token_offset,
+                       residual_grad, accumulate, dOut, X, Wqkv, Wo, QKV, P, O, dZ, dO, dP, dS, dQKV, dX, dWqkv, dbqkv,
+                       dWo, dbo, stream);
+}
+
+int qk_norm_rope_fwd(int64_t tokens, int nq, int nk, int d, int rot, int interleaved, int n_axes, int s0, int s1, int s2,
+                     float eps, const mlp_bf16* wq, const mlp_bf16* wk, const int32_t* pos, const float* inv_freq,
+                     const mlp_bf16* Q, int64_t ldq, const mlp_bf16* K, int64_t ldk, mlp_bf16* Qo, int64_t ldqo,
+                     mlp_bf16* Ko, int64_t ldko, void* stream) {
+  const char* what = "qk_norm_rope_fwd";
+  const QkRopeArgs r{rot, interleaved, n_axes, s0, s1, s2, eps, wq, wk, pos, inv_freq};
+  int rc = check_qk_rope(what, tokens, nq, nk, d, r);
+  if (!rc) rc = check_qk_rows(what, "Q", Q, ldq, nq, d);
+  if (!rc) rc = check_qk_rows(what, "K", K, ldk, nk, d);
+  if (!rc) rc = check_qk_rows(what, "Qo", Qo, ldqo, nq, d);
+  if (!rc) rc = check_qk_rows(what, "Ko", Ko, ldko, nk, d);
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  QkRopeParams p{};
+  fill_qk_rope(&p, tokens, nq, nk, d, r);
+  p.q = Q;
+  p.k = K;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.oq = Qo;
+  p.ok = Ko;
+  p.ldoq = ldqo;
+  p.ldok = ldko;
+  return launch_qk_rope(st, p, interleaved, static_cast<cudaStream_t>(stream));
+}
+
+int qk_norm_rope_bwd(int64_t tokens, int nq, int nk, int d, int rot, int interleaved, int n_axes, int s0, int s1, int s2,
+                     float eps, const mlp_bf16* wq, const mlp_bf16* wk, const int32_t* pos, const float* inv_freq,
+                     int accumulate, const mlp_bf16* Q, int64_t ldq, const mlp_bf16* K, int64_t ldk,
+                     const mlp_bf16* dQo, int64_t lddqo, const mlp_bf16* dKo, int64_t lddko, mlp_bf16* dQ, int64_t lddq,
+                     mlp_bf16* dK, int64_t lddk, float* dwq, float* dwk, float* ws, void* stream) {
+  const char* what = "qk_norm_rope_bwd";
+  const QkRopeArgs r{rot, interleaved, n_axes, s0, s1, s2, eps, wq, wk, pos, inv_freq};
+  int rc = check_qk_rope(what, tokens, nq, nk, d, r);
+  if (!rc) rc = check_qk_rows(what, "dQo", dQo, lddqo, nq, d);
+  if (!rc) rc = check_qk_rows(what, "dKo", dKo, lddko, nk, d);
+  if (!rc) rc = check_qk_rows(what, "dQ", dQ, lddq, nq, d);
+  if (!rc) rc = check_qk_rows(what, "dK", dK, lddk, nk, d);
+  if (!rc && wq != nullptr) {
+    rc = check_qk_rows(what, "Q", Q, ldq, nq, d);
+    if (!rc) rc = check_qk_rows(what, "K", K, ldk, nk, d);
+    if (!rc) rc = check_ptrs("qk_norm_rope_bwd (dwq, dwk, ws)", {dwq, dwk, ws});
+  }
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  QkRopeParams p{};
+  fill_qk_rope(&p, tokens, nq, nk, d, r);
+  p.q = Q;
+  p.k = K;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.gq = dQo;
+  p.gk = dKo;
+  p.ldgq = lddqo;
+  p.ldgk = lddko;
+  p.oq = dQ;
+  p.ok = dK;
+  p.ldoq = lddq;
+  p.ldok = lddk;
+  p.ws = ws;
+  return launch_qk_rope_bwd(st, p, interleaved, dwq, dwk, accumulate ? 1 : 0, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- gated feed-forward block
+static int check_glu(const char* what, int h, int ffn, int t, int64_t tokens, float p) {
+  const int rc = check_shape(h, ffn, t, -1, tokens, p);
+  if (rc) return rc;
+  if (ffn > (1 << 29)) return fail(MLP_EINVAL, "%s: ffn = %d is too large", what, ffn);
+  return MLP_OK;
+}
+
+static int check_glu_act(const char* what, int act) {
+  if (act != kActSilu && act != kActGelu)
+    return fail(MLP_EINVAL, "%s: act = %d is neither GLU_SILU nor GLU_GELU", what, act);
+  return MLP_OK;
+}
+
+// A pointer that may be NULL.
+static int check_opt(const char* what, const char* name, const void* p) {
+  return p == nullptr || aligned16(p) ? MLP_OK : fail(MLP_EALIGN, "%s: %s is not 16-byte aligned", what, name);
+}
+
+int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
+            const mlp_bf16* X, const mlp_bf16* A, const mlp_bf16* a, const mlp_bf16* B, const mlp_bf16* b,
+            const mlp_bf16* R, mlp_bf16* GU, mlp_bf16* Y, mlp_bf16* O, void* stream) {
+  const char* what = "glu_fwd";
+  int rc = check_glu(what, h, ffn, t, tokens, p);
+  if (!rc) rc = check_glu_act(what, act);
+  if (!rc) rc = check_ptrs(what, {X, A, B, Y, O});
+  if (!rc) rc = check_opt(what, "a", a);
+  if (!rc) rc = check_opt(what, "b", b);
+  if (!rc) rc = check_opt(what, "R", R);
+  if (!rc) rc = check_opt(what, "GU", GU);
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int T = (int)tokens;
+  if (R == nullptr) R = X;
+  rc = gemm_glu(st, X, A, a, GU, Y, T, ffn, h, act, s);
+  if (rc) return rc;
+  // O = R + dropout(Y B + b)
+  EpiParams e{};
+  e.kind = kEpiDropRes;
+  e.ld = h;
+  e.in0 = R;
+  e.bias = b;
+  e.out0 = O;
+  e.drop = make_dropout(p, seed, token_offset, h);
+  return gemm(st, Y, false, ffn, B, true, h, T, h, ffn, e, s, kTraceGluOut, false, false);
+}
+
+int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
+                  int residual_grad, const mlp_bf16* dO, const mlp_bf16* A, const mlp_bf16* B, const mlp_bf16* GU,
+                  mlp_bf16* dZ, mlp_bf16* dGU, mlp_bf16* dX, void* stream) {
+  const char* what = "glu_bwd_input";
+  int rc = check_glu(what, h, ffn, t, tokens, p);
+  if (!rc) rc = check_glu_act(what, act);
+  if (!rc) rc = check_ptrs(what, {dO, A, B, GU, dGU, dX});
+  if (!rc && p > 0.0f) rc = check_ptrs("glu_bwd_input (dZ, needed with dropout)", {dZ});
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int T = (int)tokens;
+  const mlp_bf16* g = dO;  // without dropout dZ is dO
+  if (p > 0.0f) {
+    const int64_t n = tokens * (h / 8);
+    const int64_t blocks = (n + 255) / 256 < (int64_t)st->sms * 8 ? (n + 255) / 256 : (int64_t)st->sms * 8;
+    const int ts = trace_pre(s);
+    const cudaError_t e = launch_kernel(k_dropout_bwd, dim3((unsigned)blocks), dim3(256), 0, s, 1, 1, dO, dZ, tokens, h,
+                                        make_dropout(p, seed, token_offset, h));
+    trace_post(ts, s, kTraceDropBwd, tokens, h, 0);
+    rc = launch_check(e, "dropout backward");
+    if (rc) return rc;
+    g = dZ;
+  }
+  rc = gemm_dglu(st, g, B, GU, dGU, T, ffn, h, act, s);
+  if (rc) return rc;
+  // dX = [dO +] dGU A^T: the reduction runs over both halves
+  EpiParams e{};
+  e.kind = kEpiResAdd;
+  e.ld = h;
+  e.in0 = residual_grad ? dO : nullptr;
+  e.out0 = dX;
+  return gemm(st, dGU, false, 2 * (int64_t)ffn, A, false, 2 * (int64_t)ffn, T, h, 2 * ffn, e, s, kTraceGluDX, false, false);
+}
+
+int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const mlp_bf16* X, const mlp_bf16* dZ,
+                    const mlp_bf16* Y, const mlp_bf16* dGU, float* dA, float* da, float* dB, float* db, float* scratch,
+                    void* stream) {
+  const char* what = "glu_bwd_weights";
+  int rc = check_glu(what, h, ffn, t, tokens, 0.0f);
+  if (!rc) rc = check_ptrs(what, {X, dZ, Y, dGU, dA, dB});
+  if (!rc) rc = check_opt(what, "da", da);
+  if (!rc) rc = check_opt(what, "db", db);
+  if (!rc) rc = check_opt(what, "scratch", scratch);
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int T = (int)tokens, f2 = 2 * ffn, acc = accumulate ? 1 : 0;
+  auto colsum = [&](const mlp_bf16* x, int cols, float* out) {
+    const int ts = trace_pre(s);
+    const unsigned split = colsum_split(st, cols, k_colsum_bf16);
+    const cudaError_t e =
+        launch_kernel(k_colsum_bf16, dim3((cols + kColsPerCta - 1) / kColsPerCta, split), dim3(kColThreads), 0, s, 1,
+                      split, (const uint16_t*)x, (int64_t)cols, out, tokens, cols, acc);
+    trace_post(ts, s, kTraceColsum, tokens, cols, 0);
+    return launch_check(e, "bias-gradient column sum");
+  };
+  if (da != nullptr && (rc = colsum(dGU, f2, da))) return rc;
+  if (db != nullptr && (rc = colsum(dZ, h, db))) return rc;
+  // transposed copies of X and dZ for large products, as in mlp_bwd
+  const mlp_bf16* Xt = nullptr;
+  const mlp_bf16* dZt = nullptr;
+  if (wgrad_transposed(ffn, h, tokens, scratch) && wgrad_transposed(h, f2, tokens, scratch)) {
+    mlp_bf16* x = reinterpret_cast<mlp_bf16*>(scratch);
+    mlp_bf16* z = x + (int64_t)h * tokens;
+    rc = launch_transposes(s, tokens, h, TransposeJob{X, x}, TransposeJob{dZ, z}, "transposed copies of X and dZ");
+    if (rc) return rc;
+    Xt = x;
+    dZt = z;
+  }
+  EpiParams ea{};
+  ea.kind = acc ? kEpiF32Add : kEpiF32Store;
+  ea.ld = f2;
+  ea.g_out = dA;
+  rc = Xt ? gemm(st, Xt, false, T, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false)
+          : gemm(st, X, true, h, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false);
+  if (rc) return rc;
+  EpiParams eb{};
+  eb.kind = acc ? kEpiF32Add : kEpiF32Store;
+  eb.ld = h;
+  eb.g_out = dB;
+  return dZt ? gemm(st, Y, true, ffn, dZt, false, T, ffn, h, T, eb, s, kTraceGluDW, false, false)
+             : gemm(st, Y, true, ffn, dZ, true, h, ffn, h, T, eb, s, kTraceGluDW, false, false);
 }
 
 int mlp_sync_status(void* stream) {

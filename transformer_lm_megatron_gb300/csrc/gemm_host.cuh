@@ -92,14 +92,20 @@ int operand_map(CUtensorMap* m, const void* base, bool mn_major, int64_t mn, int
   return make_map(m, base, k, mn, ld, kBK, tile_mn);
 }
 
-template <bool AM, bool BM, bool PAIR, bool BATCHED = false, bool WIDE = false>
+// static_ws: whether the launch may use the static per-stream workspaces (split tail,
+// tile counters).  The gated block's launches may not: they would tie a result's bits to
+// the stream (only the first few streams have a region) and two graphs captured on one
+// stream, which may run at once on others, to one region.
+template <bool AM, bool BM, bool PAIR, bool BATCHED = false, bool WIDE = false, int GATED = kGatedNone>
 int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC,
                   const CUtensorMap& mO0, const CUtensorMap& mO1, int M, int N, int K, const EpiParams& ep,
                   int raster_n_fast, int group, int l2_hints, cudaStream_t stream, int trace_kind, int batch = 1,
-                  int nb_h = 1, int causal = kCausalNone, bool late_wait = false) {
+                  int nb_h = 1, int causal = kCausalNone, bool late_wait = false, bool static_ws = true) {
   using Cfg = GemmCfg<PAIR, BATCHED || WIDE>;
-  auto kern = k_gemm_bf16_tc<AM, BM, PAIR, BATCHED, WIDE>;
-  const int slot = (AM ? 2 : 0) + (BM ? 1 : 0) + (PAIR ? 4 : 0) + (BATCHED ? 8 : 0) + (WIDE ? 16 : 0);
+  auto kern = k_gemm_bf16_tc<AM, BM, PAIR, BATCHED, WIDE, GATED>;
+  const int slot =
+      (AM ? 2 : 0) + (BM ? 1 : 0) + (PAIR ? 4 : 0) + (BATCHED ? 8 : 0) + (WIDE ? 16 : 0) + 32 * GATED;
+  constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;
   if (!st->gemm_attr[slot]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmemBytes);
     if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -126,7 +132,7 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
     }
     st->gemm_attr[slot] = true;
   }
-  const int64_t tiles = (int64_t)((M + Cfg::kTileM - 1) / Cfg::kTileM) * ((N + kBN - 1) / kBN) * batch;
+  const int64_t tiles = (int64_t)((M + Cfg::kTileM - 1) / Cfg::kTileM) * ((N + kTileN - 1) / kTileN) * batch;
   EpiParams epx = ep;
   epx.pace = g_epi_pace.load(std::memory_order_relaxed);
   late_wait = late_wait && g_late_wait.load(std::memory_order_relaxed) &&
@@ -141,7 +147,7 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
   epx.split_ws = nullptr;
   epx.split_flags = nullptr;
   int64_t items = tiles;
-  if (!BATCHED && !WIDE && causal == kCausalNone && !epi_f32_out(ep.kind) && !late_wait &&
+  if (!BATCHED && !WIDE && causal == kCausalNone && !epi_f32_out(ep.kind) && !late_wait && static_ws &&
       g_split_tail.load(std::memory_order_relaxed) && (K + kBK - 1) / kBK >= 16) {
     const int64_t rem = tiles % units;
     const int region = (rem > 0 && 2 * rem <= units && rem * (PAIR ? 2 : 1) * 4 <= kSplitSlots)
@@ -158,7 +164,7 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
   const int units_launched = (int)(items < units ? items : units);
   int* sched = nullptr;
   const int order = g_tile_sched.load(std::memory_order_relaxed);
-  if ((order == 1 || (order < 0 && BATCHED)) && !late_wait && items > units_launched) {
+  if ((order == 1 || (order < 0 && BATCHED)) && !late_wait && static_ws && items > units_launched) {
     const int region = split_region(st, stream);
     if (region >= 0) sched = st->sched_ctr + 2 * region;
   }
@@ -185,7 +191,8 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
 // (see k_gemm_bf16_tc); only mlp_bwd's weight-gradient and input-gradient GEMMs,
 // never the first kernel of a call.
 int gemm(DeviceState* st, const void* a, bool a_mn, int64_t lda, const void* b, bool b_mn, int64_t ldb, int M, int N,
-         int K, const EpiParams& ep, cudaStream_t stream, int trace_kind, bool late_wait = false) {
+         int K, const EpiParams& ep, cudaStream_t stream, int trace_kind, bool late_wait = false,
+         bool static_ws = true) {
   const int mode = g_pair_mode.load(std::memory_order_relaxed);
   const bool pair = mode == 1 || (mode < 0 && M > kBM);
   CUtensorMap mA, mB, mC, mO0, mO1;
@@ -233,16 +240,16 @@ int gemm(DeviceState* st, const void* a, bool a_mn, int64_t lda, const void* b, 
 #define GB_LAUNCH(AM_, BM_)                                                                                        \
   (pair ? (wide ? launch_gemm_t<AM_, BM_, true, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast,   \
                                                              group, l2_hints, stream, trace_kind, 1, 1, kCausalNone, \
-                                                             late_wait)                                              \
+                                                             late_wait, static_ws)                                   \
                 : launch_gemm_t<AM_, BM_, true, false, false>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast,  \
                                                               group, l2_hints, stream, trace_kind, 1, 1, kCausalNone,\
-                                                              late_wait))                                            \
+                                                              late_wait, static_ws))                                 \
         : (wide ? launch_gemm_t<AM_, BM_, false, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast,  \
                                                               group, l2_hints, stream, trace_kind, 1, 1, kCausalNone,\
-                                                              late_wait)                                             \
+                                                              late_wait, static_ws)                                  \
                 : launch_gemm_t<AM_, BM_, false, false, false>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, \
                                                                group, l2_hints, stream, trace_kind, 1, 1,            \
-                                                               kCausalNone, late_wait)))
+                                                               kCausalNone, late_wait, static_ws)))
   if (!a_mn && b_mn) return GB_LAUNCH(false, true);
   if (!a_mn && !b_mn) return GB_LAUNCH(false, false);
   if (a_mn && b_mn) return GB_LAUNCH(true, true);
@@ -251,8 +258,85 @@ int gemm(DeviceState* st, const void* a, bool a_mn, int64_t lda, const void* b, 
   // dZ (mlp_bwd), which always runs on CTA pairs with a deep enough reduction
   if (a_mn && !b_mn && pair && !wide)
     return launch_gemm_t<true, false, true, false, false>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, group,
-                                                          l2_hints, stream, trace_kind, 1, 1, kCausalNone, late_wait);
+                                                          l2_hints, stream, trace_kind, 1, 1, kCausalNone, late_wait,
+                                                          static_ws);
   return fail(MLP_EUNSUPPORTED, "operand layout combination not instantiated");
+}
+
+// ------------------------------------------------------- the gated block's GEMMs
+// 3-D bf16 map (column, half, row) of a [rows, 2 half_cols] tensor whose rows hold
+// two halves: out-of-range columns of the first half are not the second's.
+int make_half_map(CUtensorMap* m, const uint16_t* base, int64_t half_cols, int64_t rows, uint32_t box_cols,
+                  uint32_t box_rows, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion prom) {
+  cuuint64_t dims[3] = {(cuuint64_t)half_cols, 2, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)half_cols * 2, (cuuint64_t)half_cols * 4};
+  cuuint32_t box[3] = {box_cols, 1, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, prom, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MLP_ECUDA, "cuTensorMapEncodeTiled (two halves) failed (%d): columns %lld rows %lld", (int)r,
+                (long long)half_cols, (long long)rows);
+  return MLP_OK;
+}
+
+// G, U = X A + a and Y = act(G) U in one launch.  A [h, 2 ffn], bias a [2 ffn] or null;
+// GU [T, 2 ffn] may be null.
+int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16_t* a, uint16_t* GU, uint16_t* Y, int T,
+             int ffn, int h, int act, cudaStream_t stream) {
+  const int mode = g_pair_mode.load(std::memory_order_relaxed);
+  const bool pair = mode == 1 || (mode < 0 && T > kBM);
+  CUtensorMap mA, mB, mC, mGU, mY;
+  memset(&mC, 0, sizeof(mC));
+  int rc = operand_map(&mA, X, false, T, h, h, kBM);
+  if (!rc)
+    rc = make_half_map(&mB, A, ffn, h, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (!rc) rc = make_out_map_bf16(&mY, Y, ffn, T, ffn);
+  if (!rc)
+    rc = make_half_map(&mGU, GU ? GU : Y, GU ? ffn : 8, GU ? T : 1, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  if (rc) return rc;
+  EpiParams e{};
+  e.kind = kEpiGlu;
+  e.out0 = GU;
+  e.out1 = Y;
+  e.bias = a;
+  e.act = act;
+  const int raster_n_fast = T > 2 * (int64_t)ffn ? 1 : 0;
+  const bool wide = (h + kBK - 1) / kBK < 16;
+#define GB_GLU(PAIR_, WIDE_)                                                                                          \
+  launch_gemm_t<false, true, PAIR_, false, WIDE_, kGatedFwd>(st, mA, mB, mC, mGU, mY, T, ffn, h, e, raster_n_fast, 0, 0, \
+                                                             stream, kTraceGlu, 1, 1, kCausalNone, false, false)
+  return pair ? (wide ? GB_GLU(true, true) : GB_GLU(true, false)) : (wide ? GB_GLU(false, true) : GB_GLU(false, false));
+#undef GB_GLU
+}
+
+// dY = dZ B^T, [dG | dU] = [dY U act'(G) | dY act(G)] in one launch.  B [ffn, h].
+int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint16_t* GU, uint16_t* dGU, int T, int ffn,
+              int h, int act, cudaStream_t stream) {
+  const int mode = g_pair_mode.load(std::memory_order_relaxed);
+  const bool pair = mode == 1 || (mode < 0 && T > kBM);
+  CUtensorMap mA, mB, mC, mOut, mIn;
+  memset(&mC, 0, sizeof(mC));
+  int rc = operand_map(&mA, dZ, false, T, h, h, kBM);
+  if (!rc) rc = operand_map(&mB, B, false, ffn, h, h, pair ? GemmCfg<true>::kBLoadN : GemmCfg<false>::kBLoadN);
+  if (!rc)
+    rc = make_half_map(&mOut, dGU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  if (!rc) rc = make_half_map(&mIn, GU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  if (rc) return rc;
+  EpiParams e{};
+  e.kind = kEpiDGlu;
+  e.out0 = dGU;
+  e.in0 = GU;
+  e.act = act;
+  const int raster_n_fast = T > ffn ? 1 : 0;
+  const bool wide = (h + kBK - 1) / kBK < 16;
+#define GB_DGLU(PAIR_, WIDE_)                                                                                         \
+  launch_gemm_t<false, false, PAIR_, false, WIDE_, kGatedBwd>(st, mA, mB, mC, mOut, mIn, T, ffn, h, e, raster_n_fast, 0, \
+                                                              0, stream, kTraceDGlu, 1, 1, kCausalNone, false, false)
+  return pair ? (wide ? GB_DGLU(true, true) : GB_DGLU(true, false))
+              : (wide ? GB_DGLU(false, true) : GB_DGLU(false, false));
+#undef GB_DGLU
 }
 
 

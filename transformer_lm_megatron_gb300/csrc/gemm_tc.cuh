@@ -35,6 +35,20 @@
 //               against the producer's progress through the next tile: a burst
 //               of output stores (fp32 gradients above all) starves that tile's
 //               operand copies, and the tensor pipe with them.
+//
+// GATED: the two products of the gated feed-forward block that do not map onto a
+// plain GEMM with an element-wise epilogue.
+//   kGatedFwd  both projections G = X Ag + ag and U = X Au + au of a column block in
+//              one tile: the MMA's 256 columns are 128 columns of Ag followed by the
+//              same 128 columns of Au (of a CTA pair, the even CTA loads the gate's
+//              and the odd CTA the other's), so each epilogue thread holds both
+//              halves of its elements and forms Y = act(G) * U from the fp32
+//              accumulators.  A tile covers 128 columns of the ffn dimension.
+//   kGatedBwd  dY = dZ B^T in the accumulator, and dG = dY U act'(G),
+//              dU = dY act(G) in the epilogue from the stored G and U.
+// [G | U], its gradient and [Ag | Au] are read and written through 3-D tensor maps
+// (column, half, row), which clip each half at ffn.
+//
 // Every mbarrier wait is bounded; on timeout the kernel records kStatusTimeout in
 // the status word, drains its own copies and MMAs, frees TMEM and returns.
 #pragma once
@@ -91,6 +105,9 @@ static_assert(GemmCfg<true>::kSmemBytes <= 232448 && GemmCfg<false>::kSmemBytes 
 
 enum CausalMode : int { kCausalNone = 0, kCausalSkipUpper = 1, kCausalKUpTo = 2, kCausalKFrom = 3 };
 
+// See the file comment.
+enum GatedKind : int { kGatedNone = 0, kGatedFwd = 1, kGatedBwd = 2 };
+
 enum EpiKind : int {
   kEpiGelu = 0,      // U = acc + bias (bf16), Y = GeLU(acc + bias) (bf16)
   kEpiF32Store = 1,  // G = acc (fp32)
@@ -101,7 +118,9 @@ enum EpiKind : int {
   kEpiBias = 6,      // out = acc + bias (bf16)
   kEpiStore = 7,     // out = acc (bf16)
   kEpiScaleMask = 8,    // G = (column > row ? -inf : alpha * acc) (fp32; causal attention scores)
-  kEpiSoftmaxGrad = 9   // dS = P * (acc - delta[batch][row]) * alpha (bf16; batched; P staged by TMA)
+  kEpiSoftmaxGrad = 9,  // dS = P * (acc - delta[batch][row]) * alpha (bf16; batched; P staged by TMA)
+  kEpiGlu = 10,      // G = acc[0:128] + bias, U = acc[128:256] + bias (bf16, optional), Y = act(G) U (bf16)
+  kEpiDGlu = 11      // dG = acc U act'(G), dU = acc act(G) (bf16)
 };
 
 // Epilogues whose output is fp32 (written through the fp32 TMA map tmC).
@@ -129,6 +148,7 @@ struct EpiParams {
   const uint16_t* bias;       // bias vector indexed by output column
   float alpha;                // scale of kEpiScaleMask and kEpiSoftmaxGrad
   DropoutParams drop;
+  int act;                    // gated epilogues: the gate's activation (GluAct); bias then has two halves of N
   int pace;                   // 1: pace the output stores against the next tile's main loop
   // Split tail (bf16 epilogues of plain GEMMs): tiles [split_base, num_tiles) are
   // computed as two halves of the reduction by two CTAs (pairs); each half writes
@@ -209,7 +229,7 @@ __device__ __forceinline__ void epilogue_values(const EpiParams& ep, int64_t row
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = z[j] + v[j];
       }
-      if (col_ok) ld_bf16x8(ep.bias + col, bb);
+      if (col_ok && ep.bias != nullptr) ld_bf16x8(ep.bias + col, bb);
       if (in_box != nullptr)
         ld_staged_bf16x8(in_box, lane, g, res);
       else if (ok)
@@ -259,6 +279,57 @@ __device__ __forceinline__ void epilogue_values(const EpiParams& ep, int64_t row
   }
 }
 
+// Gated forward epilogue of one row, 32 columns [col0, col0 + 32): adds the biases to
+// G and U in place and packs Y = act(G) * U, formed from the fp32 values.
+__device__ __forceinline__ void glu_epilogue(const EpiParams& ep, int col0, int N, uint32_t (&g)[32], uint32_t (&u)[32],
+                                             uint32_t (&y)[16]) {
+  if (ep.bias != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (col0 + 8 * q >= N) continue;
+      float bg[8], bu[8];
+      ld_bf16x8(ep.bias + col0 + 8 * q, bg);
+      ld_bf16x8(ep.bias + N + col0 + 8 * q, bu);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[8 * q + j] = __float_as_uint(__uint_as_float(g[8 * q + j]) + bg[j]);
+        u[8 * q + j] = __float_as_uint(__uint_as_float(u[8 * q + j]) + bu[j]);
+      }
+    }
+  }
+  if (ep.act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      y[j] = pack_bf16x2(silu_f(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
+                         silu_f(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      y[j] = pack_bf16x2(gelu_gate_f(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
+                         gelu_gate_f(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
+  }
+}
+
+// Gated backward epilogue of one row, 32 columns: acc = dY, gp and up hold the stored
+// G and U (two bf16 per word) and receive dG = dY U act'(G) and dU = dY act(G).
+__device__ __forceinline__ void dglu_epilogue(const EpiParams& ep, const uint32_t (&acc)[32], uint32_t (&gp)[16],
+                                              uint32_t (&up)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float d0 = __uint_as_float(acc[2 * j]), d1 = __uint_as_float(acc[2 * j + 1]);
+    float v0, s0, v1, s1;
+    if (ep.act == kActSilu) {
+      silu_both_f(bf16lo(gp[j]), v0, s0);
+      silu_both_f(bf16hi(gp[j]), v1, s1);
+    } else {
+      gelu_both_f(bf16lo(gp[j]), v0, s0);
+      gelu_both_f(bf16hi(gp[j]), v1, s1);
+    }
+    gp[j] = pack_bf16x2(d0 * bf16lo(up[j]) * s0, d1 * bf16hi(up[j]) * s1);
+    up[j] = pack_bf16x2(d0 * v0, d1 * v1);
+  }
+}
+
 __device__ __forceinline__ void epilogue_dispatch(const EpiParams& ep, int64_t row, int col0, const uint32_t (&r)[32],
                                                   int M, int N, uint32_t (&o0)[16], uint32_t (&o1)[16],
                                                   const uint8_t* in_box) {
@@ -301,7 +372,7 @@ __device__ __forceinline__ void record_status(int* status, int code, int site) {
 // after the tile's last row (the result there is never read); kCausalKUpTo stops
 // each tile's reduction after its last row (A(m, k) = 0 for k > m);
 // kCausalKFrom starts it at the tile's first row (A(m, k) = 0 for k < m).
-template <bool A_MN, bool B_MN, bool PAIR, bool BATCHED, bool WIDE = false>
+template <bool A_MN, bool B_MN, bool PAIR, bool BATCHED, bool WIDE = false, int GATED = kGatedNone>
 __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
     k_gemm_bf16_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmO0,
@@ -334,7 +405,8 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
   const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;   // CTA pair or single CTA
   const int num_units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const int num_m = (M + Cfg::kTileM - 1) / Cfg::kTileM;
-  const int num_n = (N + kBN - 1) / kBN;
+  constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;   // columns of D per tile
+  const int num_n = (N + kTileN - 1) / kTileN;
   const int tiles_per_batch = num_m * num_n;
   const int num_tiles = tiles_per_batch * (BATCHED ? batch : 1);
   const int num_kb = (K + kBK - 1) / kBK;
@@ -373,7 +445,7 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
       tma_prefetch_desc(&tmC);
     } else {
       tma_prefetch_desc(&tmO0);
-      if (ep.kind == kEpiGelu || (ep.in0 != nullptr && epi_staged_input(ep.kind))) tma_prefetch_desc(&tmO1);
+      if (GATED != kGatedNone || ep.kind == kEpiGelu || (ep.in0 != nullptr && epi_staged_input(ep.kind))) tma_prefetch_desc(&tmO1);
     }
   }
   if (warp == 1) {
@@ -432,7 +504,7 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
     const int mb = raster_n_fast ? slow : fast;
     const int nb = raster_n_fast ? fast : slow;
     m0 = mb * Cfg::kTileM + (int)rank * kBM;  // this CTA's first row
-    n0 = nb * kBN;
+    n0 = nb * kTileN;
   };
   // causal structure of the batched attention products (see above); decided per
   // tile from the tile's row range, identically in every role and in both CTAs
@@ -592,7 +664,12 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
             } else {
               tma_load_2d_pair(a_dst, &tmA, bar, k0, m0, pol_a, ha != kL2None);
             }
-            if constexpr (B_MN) {
+            if constexpr (GATED == kGatedFwd) {
+              // the even CTA loads the gate's columns, the odd CTA the other half's
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tma_load_3d_pair(b_dst + j * kChunkBytes, &tmB, bar, n0 + 64 * j, (int)rank, k0);
+            } else if constexpr (B_MN) {
 #pragma unroll
               for (int j = 0; j < Cfg::kBLoadN / 64; ++j)
                 tma_load_2d_pair(b_dst + j * kChunkBytes, &tmB, bar, b_n0 + 64 * j, k0, pol_b, hb != kL2None);
@@ -608,7 +685,11 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
             } else {
               tma_load_2d(a_dst, &tmA, &full[stage], k0, m0, pol_a, ha != kL2None);
             }
-            if constexpr (B_MN) {
+            if constexpr (GATED == kGatedFwd) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tma_load_3d(b_dst + j * kChunkBytes, &tmB, &full[stage], n0 + 64 * (j & 1), j >> 1, k0);
+            } else if constexpr (B_MN) {
 #pragma unroll
               for (int j = 0; j < Cfg::kBLoadN / 64; ++j)
                 tma_load_2d(b_dst + j * kChunkBytes, &tmB, &full[stage], b_n0 + 64 * j, k0, pol_b, hb != kL2None);
@@ -717,8 +798,8 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
     const int quarter = warp & 3;
     const int row_in_tile = quarter * 32 + lane;
     // this warp's columns of each tile: all 256, or one half (8 epilogue warps)
-    const int col_begin = kEpiWarps == 8 ? ((warp - 2) >> 2) * (kBN / 2) : 0;
-    const int col_end = col_begin + kBN * 4 / kEpiWarps;
+    const int col_begin = kEpiWarps == 8 ? ((warp - 2) >> 2) * (kTileN / 2) : 0;
+    const int col_end = col_begin + kTileN * 4 / kEpiWarps;
     uint8_t* my_out = sOut + (warp - 2) * 2 * kOutBoxBytes;
     uint32_t n_out = 0;  // boxes this warp has issued
     const int hout = (l2_hints >> 4) & 3;
@@ -733,7 +814,8 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
     // kInDepth column blocks ahead, so the epilogue never waits on scattered global
     // loads.  A buffer is refilled only after the warp has read it and written its
     // output box.
-    const bool prefetch_in = ep.in0 != nullptr && epi_staged_input(ep.kind) && (!BATCHED || ep.kind == kEpiSoftmaxGrad);
+    const bool prefetch_in = GATED == kGatedNone && ep.in0 != nullptr && epi_staged_input(ep.kind) &&
+                             (!BATCHED || ep.kind == kEpiSoftmaxGrad);
     uint64_t* my_in_full = in_full + kInDepth * (warp - 2);
     uint32_t n_in = 0;  // input boxes this warp has requested
     auto in_box = [&](uint32_t i) { return my_out + (i % kInDepth) * kOutBoxBytes + kOutBoxBf16Bytes; };
@@ -745,6 +827,15 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
           tma_load_4d(in_box(n_in), &tmO1, bar, x, y, hb, sb);
         else
           tma_load_2d(in_box(n_in), &tmO1, bar, x, y, 0, false);
+      }
+      ++n_in;
+    };
+    // kGatedBwd: G and U of one column block into the warp's first two boxes
+    auto dglu_request = [&](int x, int y) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&my_in_full[0], 2 * kOutBoxBf16Bytes);
+        tma_load_3d(my_out, &tmO1, &my_in_full[0], x, 0, y);
+        tma_load_3d(my_out + kOutBoxBf16Bytes, &tmO1, &my_in_full[0], x, 1, y);
       }
       ++n_in;
     };
@@ -774,6 +865,11 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
       uint32_t n_in_used = n_in;  // index of the next input box to consume
       const int n_first = min(n_blocks, kInDepth);
       for (int q = 0; q < n_first; ++q) request_in(n0 + col_begin + 32 * q, m0 + quarter * 32, hb, sb);
+      if constexpr (GATED == kGatedBwd) {
+        // the first block's G and U; a split tail's half that turns out not to write
+        // its output (below) waits for them all the same
+        if (rows_in && n0 + col_begin < N) dglu_request(n0 + col_begin, m0 + quarter * 32);
+      }
       if (!(PAIR ? mbar_wait_cluster(&acc_full[acc], acc_phase) : mbar_wait(&acc_full[acc], acc_phase))) {
         record_status(status, kStatusTimeout, 6);
         break;
@@ -812,6 +908,10 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
         } else {
           // no output from this half: retire the input boxes requested for it
           for (int q = 0; q < n_first; ++q) wait_in(n_in_used++);
+          if constexpr (GATED == kGatedBwd) {
+            if (rows_in && n0 + col_begin < N && !mbar_wait(&my_in_full[0], (n_in - 1) & 1))
+              record_status(status, kStatusTimeout, 7);
+          }
         }
       }
       // One column block (32 columns) of this warp's rows: r holds its accumulator.
@@ -823,7 +923,8 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
           // with its operand copies in one burst.  The target is always reached (the
           // next tile's copies do not depend on this epilogue); the wait is bounded
           // all the same and only delays.
-          const uint32_t lead = min(nkb_next, (uint32_t)kStages + ((uint32_t)(c0 >> 5) * nkb_next * 3u) / 32u);
+          const uint32_t lead =
+              min(nkb_next, (uint32_t)kStages + ((uint32_t)((c0 * (kBN / kTileN)) >> 5) * nkb_next * 3u) / 32u);
           if (lane == 0) {
             const uint64_t t0 = globaltimer_ns();
             while (*kb_issued < kb_end + lead && globaltimer_ns() - t0 < kPaceLimitNs) __nanosleep(128);
@@ -831,17 +932,100 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
           __syncwarp();
         }
       };
-      auto out_block = [&](int c0, uint32_t (&r)[32]) {
-        if (other != nullptr) {
+      // the other half's partial sums of the accumulator columns [c, c + 32) (split tail)
+      auto add_other = [&](int c, uint32_t (&r)[32]) {
+        if (other == nullptr) return;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(other + c0 + 4 * j));
-            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + o.x);
-            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + o.y);
-            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + o.z);
-            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + o.w);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(other + c + 4 * j));
+          r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + o.x);
+          r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + o.y);
+          r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + o.z);
+          r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + o.w);
         }
+      };
+      // 32 packed bf16 of this lane's row into a 32 x 32 box with the 64-byte swizzle
+      auto fill_box = [&](uint8_t* box, const uint32_t (&o)[16]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      };
+      // kGatedFwd: G, U (if wanted) and Y of 32 rows x 32 columns.  Each output box
+      // leaves as a bulk group of its own through a ring of the warp's four boxes.
+      auto glu_block = [&](int c0) {
+        if (n0 + c0 >= N || m0 + quarter * 32 >= M) return;
+        uint32_t g[32], u[32], y[16];
+        tmem_ld_32x32b_x32(t_row + c0, g);
+        tmem_ld_32x32b_x32(t_row + kTileN + c0, u);
+        tmem_ld_wait();
+        add_other(c0, g);
+        add_other(kTileN + c0, u);
+        glu_epilogue(ep, n0 + c0, N, g, u, y);
+        auto put = [&](const CUtensorMap* map, int half, const uint32_t (&o)[16]) {
+          uint8_t* box = my_out + (n_out & 3) * kOutBoxBf16Bytes;
+          if (lane == 0) bulk_wait_read<3>();
+          __syncwarp();
+          fill_box(box, o);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (half < 0)
+              tma_store_2d(map, box, n0 + c0, m0 + quarter * 32, 0, false);
+            else
+              tma_store_3d(map, box, n0 + c0, half, m0 + quarter * 32);
+            bulk_commit();
+          }
+          ++n_out;
+        };
+        if (ep.out0 != nullptr) {
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+          put(&tmO0, 0, o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+          put(&tmO0, 1, o);
+        }
+        put(&tmO1, -1, y);
+      };
+      // kGatedBwd: dG and dU of 32 rows x 32 columns.  The warp's first two boxes
+      // receive the block's G and U, the other two its outputs.
+      auto dglu_block = [&](int c0) {
+        if (n0 + c0 >= N || m0 + quarter * 32 >= M) return;
+        uint32_t r[32], gp[16], up[16];
+        tmem_ld_32x32b_x32(t_row + c0, r);
+        tmem_ld_wait();
+        add_other(c0, r);
+        if (!mbar_wait(&my_in_full[0], (n_in - 1) & 1)) record_status(status, kStatusTimeout, 7);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+          const uint4 a = *reinterpret_cast<const uint4*>(my_out + off);
+          const uint4 b = *reinterpret_cast<const uint4*>(my_out + kOutBoxBf16Bytes + off);
+          gp[4 * j] = a.x, gp[4 * j + 1] = a.y, gp[4 * j + 2] = a.z, gp[4 * j + 3] = a.w;
+          up[4 * j] = b.x, up[4 * j + 1] = b.y, up[4 * j + 2] = b.z, up[4 * j + 3] = b.w;
+        }
+        if (c0 + 32 < col_end && n0 + c0 + 32 < N) {
+          fence_proxy_async_smem();  // every lane has read the boxes before they are refilled
+          __syncwarp();
+          dglu_request(n0 + c0 + 32, m0 + quarter * 32);
+        }
+        dglu_epilogue(ep, r, gp, up);  // gp, up become dG, dU
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        fill_box(my_out + 2 * kOutBoxBf16Bytes, gp);
+        fill_box(my_out + 3 * kOutBoxBf16Bytes, up);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmO0, my_out + 2 * kOutBoxBf16Bytes, n0 + c0, 0, m0 + quarter * 32);
+          tma_store_3d(&tmO0, my_out + 3 * kOutBoxBf16Bytes, n0 + c0, 1, m0 + quarter * 32);
+          bulk_commit();
+        }
+      };
+      auto out_block = [&](int c0, uint32_t (&r)[32]) {
+        add_other(c0, r);
         if (tma_out) {
           // Warp-uniform: this warp's 32 rows x 32 columns go out as one TMA box;
           // rows >= M and columns >= N are clipped by the tensor map.
@@ -940,10 +1124,16 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
 #pragma unroll 1
       for (int c0 = col_begin; c0 < (finisher ? col_end : col_begin); c0 += 32) {
         pace_block(c0);
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t_row + c0, r);
-        tmem_ld_wait();
-        out_block(c0, r);
+        if constexpr (GATED == kGatedFwd) {
+          glu_block(c0);
+        } else if constexpr (GATED == kGatedBwd) {
+          dglu_block(c0);
+        } else {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_row + c0, r);
+          tmem_ld_wait();
+          out_block(c0, r);
+        }
       }
       tc_fence_before();
       __syncwarp();

@@ -50,6 +50,15 @@ _SIGNATURES = {
     "attn_fwd": (_i32, [_i32, _i32, _i32, _i64, _i32, _f32, _u64, _u64] + [_vp] * 11 + [_vp]),
     "attn_bwd": (_i32, [_i32, _i32, _i32, _i64, _i32, _f32, _u64, _u64, _i32, _i32] + [_vp] * 17 + [_vp]),
     "mlp_fwd_static_scratch": (_i32, [_i32, _i32, _i32, _i32, _i64, _f32, _u64, _u64] + [_vp] * 6 + [_vp, _vp, _vp, _vp]),
+    "glu_fwd": (_i32, [_i32, _i32, _i32, _i64, _f32, _u64, _u64, _i32] + [_vp] * 9 + [_vp]),
+    "glu_bwd_input": (_i32, [_i32, _i32, _i32, _i64, _f32, _u64, _u64, _i32, _i32] + [_vp] * 7 + [_vp]),
+    "glu_bwd_weights": (_i32, [_i32, _i32, _i32, _i64, _i32] + [_vp] * 9 + [_vp]),
+    "qk_norm_rope_fwd": (_i32, [_i64] + [_i32] * 9 + [_f32] + [_vp] * 4 + [_vp, _i64] * 4 + [_vp]),
+    "qk_norm_rope_bwd": (_i32, [_i64] + [_i32] * 9 + [_f32] + [_vp] * 4 + [_i32] + [_vp, _i64] * 6 + [_vp] * 3 + [_vp]),
+    "attn_rope_fwd": (_i32, [_i32, _i32, _i32, _i64, _i32, _f32, _u64, _u64] + [_i32] * 6 + [_f32] + [_vp] * 4
+                      + [_vp] * 12 + [_vp]),
+    "attn_rope_bwd": (_i32, [_i32, _i32, _i32, _i64, _i32, _f32, _u64, _u64] + [_i32] * 6 + [_f32] + [_vp] * 4
+                      + [_i32, _i32] + [_vp] * 21 + [_vp]),
     "mlp_trace_begin": (_i32, [_i32]),
     "mlp_trace_end": (_i32, [_i32, _vp, _vp, _vp]),
 }
@@ -157,6 +166,170 @@ def attn_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, residual_grad, ac
                            _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# Gated feed-forward block, head norms and rotation.  These check the tensors they
+# are given (type, shape, device) before their pointers go to the library.
+# ---------------------------------------------------------------------------
+GLU_SILU, GLU_GELU = 0, 1
+
+
+def _arg(name, t, dtype, shape, optional=False):
+    """The pointer of a contiguous tensor of this type and shape on the current device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    p = _ptr(t)
+    _check_device(name, t)
+    return p
+
+
+def _check_device(name, t):
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
+
+
+def _rows(name, t, tokens, heads, d):
+    """(pointer, row stride) of a [tokens, heads, d] tensor whose heads lie side by side."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be torch.bfloat16 {(tokens, heads, d)}, not {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    _check_device(name, t)
+    if t.stride(2) != 1 and d > 1 or t.stride(1) != d and heads > 1:
+        raise ValueError(f"{name}: a token's heads must lie side by side, strides are {t.stride()}")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
+
+
+def glu_fwd(h, ffn, t, tokens, p, seed, token_offset, act, X, A, a, B, b, R, GU, Y, O, stream=None):
+    """Forward of the gated feed-forward block (see include/gb_mlp.h): O = R + dropout((act(G) U) B + b);
+    a, b, R and GU may be None."""
+    bf = torch.bfloat16
+    _check(load().glu_fwd(h, ffn, t, tokens, p, seed, token_offset, act, _arg("X", X, bf, (tokens, h)),
+                          _arg("A", A, bf, (h, 2 * ffn)), _arg("a", a, bf, (2 * ffn,), True),
+                          _arg("B", B, bf, (ffn, h)), _arg("b", b, bf, (h,), True),
+                          _arg("R", R, bf, (tokens, h), True), _arg("GU", GU, bf, (tokens, 2 * ffn), True),
+                          _arg("Y", Y, bf, (tokens, ffn)), _arg("O", O, bf, (tokens, h)), _stream(stream)))
+
+
+def glu_bwd_input(h, ffn, t, tokens, p, seed, token_offset, act, residual_grad, dO, A, B, GU, dZ, dGU, dX, stream=None):
+    """dZ, dGU = [dG | dU] and dX of the gated block; dZ may be None where p = 0 (dZ is then dO)."""
+    bf = torch.bfloat16
+    _check(load().glu_bwd_input(h, ffn, t, tokens, p, seed, token_offset, act, int(residual_grad),
+                                _arg("dO", dO, bf, (tokens, h)), _arg("A", A, bf, (h, 2 * ffn)),
+                                _arg("B", B, bf, (ffn, h)), _arg("GU", GU, bf, (tokens, 2 * ffn)),
+                                _arg("dZ", dZ, bf, (tokens, h), p == 0), _arg("dGU", dGU, bf, (tokens, 2 * ffn)),
+                                _arg("dX", dX, bf, (tokens, h)), _stream(stream)))
+
+
+def glu_bwd_weights(h, ffn, t, tokens, accumulate, X, dZ, Y, dGU, dA, da, dB, db, scratch=None, stream=None):
+    """dA, da, dB, db (fp32) of the gated block from what the forward and glu_bwd_input stored; da, db and
+    scratch may be None."""
+    bf, f32 = torch.bfloat16, torch.float32
+    _check(load().glu_bwd_weights(h, ffn, t, tokens, int(accumulate), _arg("X", X, bf, (tokens, h)),
+                                  _arg("dZ", dZ, bf, (tokens, h)), _arg("Y", Y, bf, (tokens, ffn)),
+                                  _arg("dGU", dGU, bf, (tokens, 2 * ffn)), _arg("dA", dA, f32, (h, 2 * ffn)),
+                                  _arg("da", da, f32, (2 * ffn,), True), _arg("dB", dB, f32, (ffn, h)),
+                                  _arg("db", db, f32, (h,), True), _arg("scratch", scratch, f32, (tokens, h), True),
+                                  _stream(stream)))
+
+
+def qk_norm_rope_workspace(d: int) -> int:
+    """Floats of qk_norm_rope_bwd's and attn_rope_bwd's workspace for heads of size d."""
+    return 1024 * 2 * d
+
+
+def _rope_args(tokens, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps):
+    rot = d if rot is None else rot
+    sections = [rot // 2] if sections is None else list(sections)
+    if not 1 <= len(sections) <= 3:
+        raise ValueError(f"one to three sections, not {len(sections)}")
+    s = sections + [0] * (3 - len(sections))
+    return (rot, int(interleaved), len(sections), *s, eps, _arg("wq", wq, torch.bfloat16, (d,), True),
+            _arg("wk", wk, torch.bfloat16, (d,), True), _arg("pos", pos, torch.int32, (len(sections), tokens)),
+            _arg("inv_freq", inv_freq, torch.float32, (rot // 2,)))
+
+
+def qk_norm_rope_fwd(Q, K, Qo, Ko, pos, inv_freq, wq=None, wk=None, eps=1e-6, rot=None, sections=None,
+                     interleaved=False, stream=None):
+    """Head norms (with weights wq, wk; none without) and rotation of Q [tokens, nq, d] and K [tokens, nk, d] into
+    Qo and Ko.  pos [axes, tokens] int32, inv_freq [rot / 2] fp32, sections: the pairs of each axis."""
+    T, nq, d = Q.shape
+    nk = K.shape[1]
+    q, k, qo, ko = (_rows(n, x, T, heads, d) for n, x, heads in (("Q", Q, nq), ("K", K, nk), ("Qo", Qo, nq), ("Ko", Ko, nk)))
+    _check(load().qk_norm_rope_fwd(T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps),
+                                   *q, *k, *qo, *ko, _stream(stream)))
+
+
+def qk_norm_rope_bwd(Q, K, dQo, dKo, dQ, dK, pos, inv_freq, wq=None, wk=None, dwq=None, dwk=None, ws=None, eps=1e-6,
+                     rot=None, sections=None, interleaved=False, accumulate=True, stream=None):
+    """Gradients dQ, dK of qk_norm_rope_fwd from dQo, dKo, and with the norm dwq, dwk [d] fp32 (ws: fp32 workspace of
+    qk_norm_rope_workspace(d) floats).  Without the norm Q and K may be None."""
+    T, nq, d = dQo.shape
+    nk = dKo.shape[1]
+    g = [_rows(n, x, T, heads, d) for n, x, heads in (("dQo", dQo, nq), ("dKo", dKo, nk), ("dQ", dQ, nq), ("dK", dK, nk))]
+    x = [(None, 0), (None, 0)]
+    if wq is not None:
+        x = [_rows("Q", Q, T, nq, d), _rows("K", K, T, nk, d)]
+    _check(load().qk_norm_rope_bwd(T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps),
+                                   int(accumulate), *x[0], *x[1], *g[0], *g[1], *g[2], *g[3],
+                                   *_dw_args(d, wq, dwq, dwk, ws), _stream(stream)))
+
+
+def _dw_args(d, wq, dwq, dwk, ws):
+    if wq is None:
+        return None, None, None
+    f32 = torch.float32
+    return (_arg("dwq", dwq, f32, (d,)), _arg("dwk", dwk, f32, (d,)), _arg("ws", ws, f32, (qk_norm_rope_workspace(d),)))
+
+
+class Rope:
+    """Norm and rotation of an attention block's queries and keys: what attn_rope_fwd and attn_rope_bwd take besides
+    the block's own tensors.  pos [axes, tokens] int32, inv_freq [rot / 2] fp32; wq, wk [d] bf16 or None; dwq, dwk
+    [d] fp32 and the workspace are made here."""
+
+    def __init__(self, d, pos, inv_freq, wq=None, wk=None, eps=1e-6, rot=None, sections=None, interleaved=False):
+        self.d, self.pos, self.inv_freq, self.wq, self.wk, self.eps = d, pos, inv_freq, wq, wk, eps
+        self.rot, self.sections, self.interleaved = rot, sections, interleaved
+        self.dwq = self.dwk = self.ws = None
+        if wq is not None:
+            f32 = dict(dtype=torch.float32, device=pos.device)
+            self.dwq, self.dwk = torch.zeros(d, **f32), torch.zeros(d, **f32)
+            self.ws = torch.empty(qk_norm_rope_workspace(d), **f32)
+
+    def args(self, tokens):
+        return _rope_args(tokens, self.d, self.pos, self.inv_freq, self.wq, self.wk, self.rot, self.sections,
+                          self.interleaved, self.eps)
+
+
+def attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, X, Wqkv, bqkv, Wo, bo, R, QKV, QKr, S, P, O,
+                  out, stream=None):
+    """attn_fwd with the norms and rotation of ``rope`` (a Rope) on its queries and keys; QKr [tokens, 2h] holds them."""
+    bf = torch.bfloat16
+    pshape = (tokens // seq_len, nh, seq_len, seq_len)
+    _check(load().attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens),
+                                _arg("X", X, bf, (tokens, h)), _arg("Wqkv", Wqkv, bf, (h, 3 * h)),
+                                _arg("bqkv", bqkv, bf, (3 * h,)), _arg("Wo", Wo, bf, (h, h)), _arg("bo", bo, bf, (h,)),
+                                _arg("R", R, bf, (tokens, h), True), _arg("QKV", QKV, bf, (tokens, 3 * h)),
+                                _arg("QKr", QKr, bf, (tokens, 2 * h)), _arg("S", S, torch.float32, pshape),
+                                _arg("P", P, bf, pshape), _arg("O", O, bf, (tokens, h)),
+                                _arg("out", out, bf, (tokens, h)), _stream(stream)))
+
+
+def attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, residual_grad, accumulate, dOut, X, Wqkv, Wo,
+                  QKV, QKr, P, O, dZ, dO, dP, dS, dQKV, dX, dWqkv, dbqkv, dWo, dbo, stream=None):
+    """attn_bwd of attn_rope_fwd; rope.dwq and rope.dwk receive the norm weights' gradients."""
+    _check(load().attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens),
+                                int(residual_grad), int(accumulate), _ptr(dOut), _ptr(X), _ptr(Wqkv), _ptr(Wo), _ptr(QKV),
+                                _arg("QKr", QKr, torch.bfloat16, (tokens, 2 * h)), _ptr(P), _ptr(O), _ptr(dZ), _ptr(dO),
+                                _ptr(dP), _ptr(dS), _ptr(dQKV), _ptr(dX), _ptr(dWqkv), _ptr(dbqkv), _ptr(dWo), _ptr(dbo),
+                                *_dw_args(rope.d, rope.wq, rope.dwq, rope.dwk, rope.ws), _stream(stream)))
+
+
 class AttnBuffers:
     """Saved activations, workspaces and fp32 gradients of the attention block."""
 
@@ -245,7 +418,10 @@ TRACE_NAMES = {0: "F1 gemm X.A_i +a, GeLU", 1: "F2 gemm Y_i.B_i (+dropout,+resid
                3: "B3 gemm Y_i^T.dZ (+= dB)", 4: "B4 gemm X^T.dU_i (+= dA)", 5: "B5 gemm dU_i.A_i^T (+dO)",
                10: "dropout backward + db", 11: "column sum da", 12: "accumulator reset", 14: "adam step",
                15: "transposed copies X^T, dZ^T",
-               20: "attention GEMM", 21: "softmax, softmax-grad row sums", 22: "fused attention core"}
+               20: "attention GEMM", 21: "softmax, softmax-grad row sums", 22: "fused attention core",
+           30: "gated block X.[Ag|Au], gate", 31: "gated block Y.B (+dropout,+residual)",
+           32: "gated block dZ.B^T, gate gradient", 33: "gated block dGU.A^T (+dO)", 34: "gated block weight gradients",
+           40: "head norms, rotation", 41: "head norms, rotation backward", 42: "head norm weight gradients"}
 GEMM_KINDS = (0, 1, 2, 3, 4, 5)
 
 
