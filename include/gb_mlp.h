@@ -270,8 +270,7 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
  *   elements apart (a multiple of 8, at least heads * d): the queries and keys inside a
  *   fused projection's output, for instance.  An output may be the same memory as an
  *   input (same pointer and ld); otherwise they may not overlap.
- * Angles are exact to 2^-30 of a turn for positions up to 2^22, and to 2^-21 of a
- * turn for any.
+ * Angles are exact to 2^-30 of a turn for any position, where |inv_freq| <= 1.
  * Backward: dwq, dwk [d] fp32 are added to (accumulate = 1) or overwritten (0); ws is
  * an fp32 workspace of QK_NORM_ROPE_WS_ROWS * 2 * d floats.  Without the norm (wq and
  * wk NULL) Q, K, dwq, dwk and ws are not used and may be NULL.  Deterministic.

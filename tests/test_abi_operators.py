@@ -115,8 +115,9 @@ def test_valid_calls_without_a_gpu_report_unsupported(lib):
     assert lib.glu_bwd_weights(*{**GLU_W, **dict(da=None, db=None, scratch=None)}.values()) == EUNS
 
 
-def test_binding_refuses_wrong_tensors():
+def test_binding_refuses_wrong_tensors(monkeypatch):
     """Types, shapes, layouts and places, before the library sees a pointer."""
+    monkeypatch.setattr(mlp, "_device", lambda: 0)
     bf = dict(dtype=torch.bfloat16)
     T, h, f = 4, 16, 24
     good = dict(X=torch.zeros(T, h, **bf), A=torch.zeros(h, 2 * f, **bf), a=None, B=torch.zeros(f, h, **bf), b=None, R=None, GU=None,
@@ -133,18 +134,42 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(ValueError):
             mlp.qk_norm_rope_fwd(q, Q, qo, Q, pos, inv)
     with pytest.raises(ValueError):
-        mlp._rope_args(T, 16, pos, inv, None, None, None, [2, 2, 2, 2], False, 1e-6)
+        mlp._rope_args(T, 16, pos, inv, None, None, None, [2, 2, 2, 2], False, 1e-6, 0)
     with pytest.raises(ValueError):
-        mlp._rope_args(T, 16, pos.long(), inv, None, None, None, None, False, 1e-6)
+        mlp._rope_args(T, 16, pos.long(), inv, None, None, None, None, False, 1e-6, 0)
 
 
-def test_binding_refuses_another_device(monkeypatch):
+class _Fake:
+    """A tensor of another device, for machines without one."""
+    dtype, is_cuda, device = torch.bfloat16, True, torch.device("cuda", 1)
+
+    def __init__(self, *shape, strides=None):
+        self.shape, self.strides = torch.Size(shape), strides
+
+    def get_device(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return self.strides
+
+    def data_ptr(self):
+        return GOOD
+
+
+def test_binding_refuses_another_device_and_other_strides():
     """A tensor of a device that is not the current one is refused: the launch would go to the current one's stream."""
-    class Elsewhere:
-        device = torch.device("cuda", 1)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
-        mlp._check_device("X", Elsewhere())
+        mlp._arg("X", _Fake(4, 16), torch.bfloat16, (4, 16), 0)
+    with pytest.raises(ValueError, match="current device"):
+        mlp._rows("Q", _Fake(4, 2, 16, strides=(32, 16, 1)), (4, 2, 16), 0)
+    assert mlp._rows("Q", _Fake(4, 2, 16, strides=(96, 16, 1)), (4, 2, 16), 1) == (GOOD, 96)
+    assert mlp._rows("Q", _Fake(1, 2, 16, strides=(7, 16, 1)), (1, 2, 16), 1) == (GOOD, 32)   # one row: no stride
+    for strides in ((96, 48, 1), (96, 16, 2), (1, 4, 8)):
+        with pytest.raises(ValueError, match="side by side"):
+            mlp._rows("Q", _Fake(4, 2, 16, strides=strides), (4, 2, 16), 1)
 
 
 def test_workspace_size_matches_the_header():

@@ -185,8 +185,8 @@ def test_in_place(norm):
 
 
 def test_positions_at_the_ends_of_their_type():
-    """Any int32 position: the angle is the exact product modulo a turn, off by the frequency's 2^-53 of
-    a turn times the position, 2^-22 turns or 1.5e-6 radians."""
+    """Any int32 position: the angle is the exact product modulo a turn, off by the frequency's 2^-64 of a
+    turn times the position and by the 2^-32 of a turn that its top 32 bits leave out."""
     c = Case(6, 2, 2, 64, norm=False)
     c.pos = torch.tensor([[0, 2**31 - 1, -2**31, 2**24 + 1, -1, 123456789]], dtype=torch.int32, device="cuda")
     (Qo, _), (Ko, _) = c.out(2), c.out(2)

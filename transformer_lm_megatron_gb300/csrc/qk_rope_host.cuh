@@ -66,63 +66,61 @@ void fill_qk_rope(QkRopeParams* p, int64_t tokens, int nq, int nk, int d, const 
   p->inv_freq = r.inv_freq;
 }
 
-// The share of a warp: one token's heads, or fewer while that leaves warps idle.
+// The steps of a token, and the grid: a step for each warp, at most ctas_per_sm CTAs an SM.
 unsigned plan_qk_rope(const DeviceState* st, QkRopeParams* p, int vec, int ctas_per_sm) {
-  const int hpw = 32 / (p->d / (2 * vec)), heads = p->nq + p->nk;
-  const int64_t warps = (int64_t)st->sms * ctas_per_sm * kQkWarps;
-  const int steps = (heads + hpw - 1) / hpw;  // a warp's steps over one token
-  int64_t units = warps / p->tokens;
-  if (units < 1) units = 1;
-  if (units > steps) units = steps;
-  p->heads_per_unit = (int)((steps + units - 1) / units) * hpw;
-  p->units = (heads + p->heads_per_unit - 1) / p->heads_per_unit;
-  const int64_t ctas = (p->tokens * p->units + kQkWarps - 1) / kQkWarps;
-  return (unsigned)(ctas < (int64_t)st->sms * ctas_per_sm ? ctas : (int64_t)st->sms * ctas_per_sm);
+  const int hpw = 32 / (p->d / (2 * vec));
+  p->steps_q = (p->nq + hpw - 1) / hpw;
+  p->steps_k = (p->nk + hpw - 1) / hpw;
+  const int64_t ctas = (p->tokens * (p->steps_q + p->steps_k) + kQkWarps - 1) / kQkWarps;
+  const int64_t most = (int64_t)st->sms * ctas_per_sm;
+  return (unsigned)(ctas < most ? ctas : most);
 }
 
 bool qk_wide(int d, int rot) { return d % 16 == 0 && rot % 16 == 0; }  // vectors of 8 elements, else 4
 
-int launch_qk_rope(DeviceState* st, QkRopeParams p, int interleaved, cudaStream_t s) {
-  const int vec = qk_wide(p.d, p.rot) ? 8 : 4;
-  const unsigned grid = plan_qk_rope(st, &p, vec, 4);
-  const bool norm = p.wq != nullptr;
-  const int ts = trace_pre(s);
-  cudaError_t e;
-#define GB_QK(V_, I_, N_) e = launch_kernel(k_qk_norm_rope<V_, I_, N_>, dim3(grid), dim3(kQkThreads), 0, s, 1, 1, p)
-  if (vec == 8) {
-    if (interleaved) { if (norm) GB_QK(8, true, true); else GB_QK(8, true, false); }
-    else { if (norm) GB_QK(8, false, true); else GB_QK(8, false, false); }
-  } else {
-    if (interleaved) { if (norm) GB_QK(4, true, true); else GB_QK(4, true, false); }
-    else { if (norm) GB_QK(4, false, true); else GB_QK(4, false, false); }
+template <int VEC, bool INTER, bool NORM, bool BWD>
+int launch_qk_t(DeviceState* st, QkRopeParams& p, cudaStream_t s, unsigned* ctas) {
+  auto kern = k_qk_norm_rope<VEC, INTER, NORM, BWD>;
+  constexpr int smem = QkSmem<VEC, BWD, NORM>::kBytes;
+  int& per_sm = st->qk_per_sm[(VEC == 8 ? 8 : 0) + (INTER ? 4 : 0) + (NORM ? 2 : 0) + (BWD ? 1 : 0)];
+  if (per_sm == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kQkThreads, smem);
+    if (e != cudaSuccess || n < 1) return fail(MLP_ECUDA, "head norms and rotation: %s", cudaGetErrorString(e));
+    per_sm = n < kQkMaxPerSm ? n : kQkMaxPerSm;
   }
-#undef GB_QK
-  trace_post(ts, s, kTraceQkRope, p.tokens, (int64_t)(p.nq + p.nk) * p.d, 0);
+  *ctas = plan_qk_rope(st, &p, VEC, per_sm);
+  const int ts = trace_pre(s);
+  const cudaError_t e = launch_kernel(kern, dim3(*ctas), dim3(kQkThreads), smem, s, 1, 1, p);
+  trace_post(ts, s, BWD ? kTraceQkRopeBwd : kTraceQkRope, p.tokens, (int64_t)(p.nq + p.nk) * p.d, 0);
   return launch_check(e, "head norms and rotation");
+}
+
+template <bool BWD>
+int launch_qk(DeviceState* st, QkRopeParams& p, int interleaved, cudaStream_t s, unsigned* ctas) {
+  const bool norm = p.wq != nullptr;
+  if (qk_wide(p.d, p.rot)) {
+    if (interleaved) return norm ? launch_qk_t<8, true, true, BWD>(st, p, s, ctas) : launch_qk_t<8, true, false, BWD>(st, p, s, ctas);
+    return norm ? launch_qk_t<8, false, true, BWD>(st, p, s, ctas) : launch_qk_t<8, false, false, BWD>(st, p, s, ctas);
+  }
+  if (interleaved) return norm ? launch_qk_t<4, true, true, BWD>(st, p, s, ctas) : launch_qk_t<4, true, false, BWD>(st, p, s, ctas);
+  return norm ? launch_qk_t<4, false, true, BWD>(st, p, s, ctas) : launch_qk_t<4, false, false, BWD>(st, p, s, ctas);
+}
+
+int launch_qk_rope(DeviceState* st, QkRopeParams p, int interleaved, cudaStream_t s) {
+  unsigned ctas = 0;
+  return launch_qk<false>(st, p, interleaved, s, &ctas);
 }
 
 int launch_qk_rope_bwd(DeviceState* st, QkRopeParams p, int interleaved, float* dwq, float* dwk, int accumulate,
                        cudaStream_t s) {
-  const int vec = qk_wide(p.d, p.rot) ? 8 : 4;
-  const unsigned grid = plan_qk_rope(st, &p, vec, 4);
-  const bool norm = p.wq != nullptr;
+  unsigned ctas = 0;
+  const int rc = launch_qk<true>(st, p, interleaved, s, &ctas);
+  if (rc || p.wq == nullptr) return rc;
   const int ts = trace_pre(s);
-  cudaError_t e;
-#define GB_QK(V_, I_, N_) e = launch_kernel(k_qk_norm_rope_bwd<V_, I_, N_>, dim3(grid), dim3(kQkThreads), 0, s, 1, 1, p)
-  if (vec == 8) {
-    if (interleaved) { if (norm) GB_QK(8, true, true); else GB_QK(8, true, false); }
-    else { if (norm) GB_QK(8, false, true); else GB_QK(8, false, false); }
-  } else {
-    if (interleaved) { if (norm) GB_QK(4, true, true); else GB_QK(4, true, false); }
-    else { if (norm) GB_QK(4, false, true); else GB_QK(4, false, false); }
-  }
-#undef GB_QK
-  trace_post(ts, s, kTraceQkRopeBwd, p.tokens, (int64_t)(p.nq + p.nk) * p.d, 0);
-  int rc = launch_check(e, "head norms and rotation backward");
-  if (rc || !norm) return rc;
-  const int tw = trace_pre(s);
-  e = launch_kernel(k_qk_dw, dim3((2 * p.d + 31) / 32), dim3(1024), 0, s, 1, 1, (const float*)p.ws, (int)grid, p.d, dwq,
-                    dwk, accumulate);
-  trace_post(tw, s, kTraceQkDw, grid, 2 * p.d, 0);
+  const cudaError_t e = launch_kernel(k_qk_dw, dim3((2 * p.d + 31) / 32), dim3(1024), 0, s, 1, 1, (const float*)p.ws,
+                                      (int)ctas, p.d, dwq, dwk, accumulate);
+  trace_post(ts, s, kTraceQkDw, ctas, 2 * p.d, 0);
   return launch_check(e, "head norm weight gradients");
 }

@@ -168,74 +168,90 @@ def attn_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, residual_grad, ac
 
 # ---------------------------------------------------------------------------
 # Gated feed-forward block, head norms and rotation.  These check the tensors they
-# are given (type, shape, device) before their pointers go to the library.
+# are given (type, shape, device) before their pointers go to the library.  A single
+# token's launch takes a few microseconds, so the checks are a few attribute reads a
+# tensor, and what is wrong is worked out only once something is.
 # ---------------------------------------------------------------------------
 GLU_SILU, GLU_GELU = 0, 1
+_bf16, _float, _int = torch.bfloat16, torch.float32, torch.int32
+_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _arg(name, t, dtype, shape, optional=False):
-    """The pointer of a contiguous tensor of this type and shape on the current device."""
+def _here(dev, stream):
+    """The stream of a call on device ``dev``: the given one, or torch's current one there."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _refuse(name, t, dtype, shape, dev):
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    p = _ptr(t)
-    _check_device(name, t)
-    return p
-
-
-def _check_device(name, t):
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
-
-
-def _rows(name, t, tokens, heads, d):
-    """(pointer, row stride) of a [tokens, heads, d] tensor whose heads lie side by side."""
-    if t is None:
-        raise ValueError(f"{name} is missing")
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (tokens, heads, d):
-        raise ValueError(f"{name} must be torch.bfloat16 {(tokens, heads, d)}, not {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    _check_device(name, t)
-    if t.stride(2) != 1 and d > 1 or t.stride(1) != d and heads > 1:
-        raise ValueError(f"{name}: a token's heads must lie side by side, strides are {t.stride()}")
-    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device {dev}")
+    raise ValueError(f"{name} must be contiguous (a token's heads side by side), its strides are {t.stride()}")
+
+
+def _arg(name, t, dtype, shape, dev):
+    """The pointer of a contiguous tensor of this type and shape on the current device ``dev``."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape, dev):
+    return None if t is None else _arg(name, t, dtype, shape, dev)
+
+
+def _rows(name, t, shape, dev):
+    """(pointer, row stride) of a [tokens, heads, d] bf16 tensor whose heads lie side by side."""
+    if t is None or t.dtype is not _bf16 or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, _bf16, shape, dev)
+    row, head, one = t.stride()
+    tokens, heads, d = shape
+    if one != 1 and d > 1 or head != d and heads > 1:
+        _refuse(name, t, _bf16, shape, dev)
+    return t.data_ptr(), row if tokens > 1 else heads * d
 
 
 def glu_fwd(h, ffn, t, tokens, p, seed, token_offset, act, X, A, a, B, b, R, GU, Y, O, stream=None):
     """Forward of the gated feed-forward block (see include/gb_mlp.h): O = R + dropout((act(G) U) B + b);
     a, b, R and GU may be None."""
-    bf = torch.bfloat16
-    _check(load().glu_fwd(h, ffn, t, tokens, p, seed, token_offset, act, _arg("X", X, bf, (tokens, h)),
-                          _arg("A", A, bf, (h, 2 * ffn)), _arg("a", a, bf, (2 * ffn,), True),
-                          _arg("B", B, bf, (ffn, h)), _arg("b", b, bf, (h,), True),
-                          _arg("R", R, bf, (tokens, h), True), _arg("GU", GU, bf, (tokens, 2 * ffn), True),
-                          _arg("Y", Y, bf, (tokens, ffn)), _arg("O", O, bf, (tokens, h)), _stream(stream)))
+    dev, rows = _device(), (tokens, h)
+    _check(load().glu_fwd(h, ffn, t, tokens, p, seed, token_offset, act, _arg("X", X, _bf16, rows, dev),
+                          _arg("A", A, _bf16, (h, 2 * ffn), dev), _opt("a", a, _bf16, (2 * ffn,), dev),
+                          _arg("B", B, _bf16, (ffn, h), dev), _opt("b", b, _bf16, (h,), dev),
+                          _opt("R", R, _bf16, rows, dev), _opt("GU", GU, _bf16, (tokens, 2 * ffn), dev),
+                          _arg("Y", Y, _bf16, (tokens, ffn), dev), _arg("O", O, _bf16, rows, dev), _here(dev, stream)))
 
 
 def glu_bwd_input(h, ffn, t, tokens, p, seed, token_offset, act, residual_grad, dO, A, B, GU, dZ, dGU, dX, stream=None):
     """dZ, dGU = [dG | dU] and dX of the gated block; dZ may be None where p = 0 (dZ is then dO)."""
-    bf = torch.bfloat16
+    dev, rows, gates = _device(), (tokens, h), (tokens, 2 * ffn)
+    if dZ is None and p != 0:
+        raise ValueError("dZ is missing (needed with dropout)")
     _check(load().glu_bwd_input(h, ffn, t, tokens, p, seed, token_offset, act, int(residual_grad),
-                                _arg("dO", dO, bf, (tokens, h)), _arg("A", A, bf, (h, 2 * ffn)),
-                                _arg("B", B, bf, (ffn, h)), _arg("GU", GU, bf, (tokens, 2 * ffn)),
-                                _arg("dZ", dZ, bf, (tokens, h), p == 0), _arg("dGU", dGU, bf, (tokens, 2 * ffn)),
-                                _arg("dX", dX, bf, (tokens, h)), _stream(stream)))
+                                _arg("dO", dO, _bf16, rows, dev), _arg("A", A, _bf16, (h, 2 * ffn), dev),
+                                _arg("B", B, _bf16, (ffn, h), dev), _arg("GU", GU, _bf16, gates, dev),
+                                _opt("dZ", dZ, _bf16, rows, dev), _arg("dGU", dGU, _bf16, gates, dev),
+                                _arg("dX", dX, _bf16, rows, dev), _here(dev, stream)))
 
 
 def glu_bwd_weights(h, ffn, t, tokens, accumulate, X, dZ, Y, dGU, dA, da, dB, db, scratch=None, stream=None):
     """dA, da, dB, db (fp32) of the gated block from what the forward and glu_bwd_input stored; da, db and
     scratch may be None."""
-    bf, f32 = torch.bfloat16, torch.float32
-    _check(load().glu_bwd_weights(h, ffn, t, tokens, int(accumulate), _arg("X", X, bf, (tokens, h)),
-                                  _arg("dZ", dZ, bf, (tokens, h)), _arg("Y", Y, bf, (tokens, ffn)),
-                                  _arg("dGU", dGU, bf, (tokens, 2 * ffn)), _arg("dA", dA, f32, (h, 2 * ffn)),
-                                  _arg("da", da, f32, (2 * ffn,), True), _arg("dB", dB, f32, (ffn, h)),
-                                  _arg("db", db, f32, (h,), True), _arg("scratch", scratch, f32, (tokens, h), True),
-                                  _stream(stream)))
+    dev, rows = _device(), (tokens, h)
+    _check(load().glu_bwd_weights(h, ffn, t, tokens, int(accumulate), _arg("X", X, _bf16, rows, dev),
+                                  _arg("dZ", dZ, _bf16, rows, dev), _arg("Y", Y, _bf16, (tokens, ffn), dev),
+                                  _arg("dGU", dGU, _bf16, (tokens, 2 * ffn), dev),
+                                  _arg("dA", dA, _float, (h, 2 * ffn), dev), _opt("da", da, _float, (2 * ffn,), dev),
+                                  _arg("dB", dB, _float, (ffn, h), dev), _opt("db", db, _float, (h,), dev),
+                                  _opt("scratch", scratch, _float, rows, dev), _here(dev, stream)))
 
 
 def qk_norm_rope_workspace(d: int) -> int:
@@ -243,48 +259,51 @@ def qk_norm_rope_workspace(d: int) -> int:
     return 1024 * 2 * d
 
 
-def _rope_args(tokens, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps):
-    rot = d if rot is None else rot
-    sections = [rot // 2] if sections is None else list(sections)
-    if not 1 <= len(sections) <= 3:
-        raise ValueError(f"one to three sections, not {len(sections)}")
-    s = sections + [0] * (3 - len(sections))
-    return (rot, int(interleaved), len(sections), *s, eps, _arg("wq", wq, torch.bfloat16, (d,), True),
-            _arg("wk", wk, torch.bfloat16, (d,), True), _arg("pos", pos, torch.int32, (len(sections), tokens)),
-            _arg("inv_freq", inv_freq, torch.float32, (rot // 2,)))
+def _rope_args(tokens, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev):
+    if rot is None:
+        rot = d
+    if sections is None:
+        sections = (rot // 2,)
+    axes = len(sections)
+    if not 1 <= axes <= 3:
+        raise ValueError(f"one to three sections, not {axes}")
+    return (rot, 1 if interleaved else 0, axes, sections[0], sections[1] if axes > 1 else 0, sections[2] if axes > 2 else 0,
+            eps, _opt("wq", wq, _bf16, (d,), dev), _opt("wk", wk, _bf16, (d,), dev), _arg("pos", pos, _int, (axes, tokens), dev),
+            _arg("inv_freq", inv_freq, _float, (rot // 2,), dev))
+
+
+def _dw_args(d, wq, dwq, dwk, ws, dev):
+    if wq is None:
+        return None, None, None
+    return (_arg("dwq", dwq, _float, (d,), dev), _arg("dwk", dwk, _float, (d,), dev),
+            _arg("ws", ws, _float, (qk_norm_rope_workspace(d),), dev))
 
 
 def qk_norm_rope_fwd(Q, K, Qo, Ko, pos, inv_freq, wq=None, wk=None, eps=1e-6, rot=None, sections=None,
                      interleaved=False, stream=None):
     """Head norms (with weights wq, wk; none without) and rotation of Q [tokens, nq, d] and K [tokens, nk, d] into
     Qo and Ko.  pos [axes, tokens] int32, inv_freq [rot / 2] fp32, sections: the pairs of each axis."""
-    T, nq, d = Q.shape
-    nk = K.shape[1]
-    q, k, qo, ko = (_rows(n, x, T, heads, d) for n, x, heads in (("Q", Q, nq), ("K", K, nk), ("Qo", Qo, nq), ("Ko", Ko, nk)))
-    _check(load().qk_norm_rope_fwd(T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps),
-                                   *q, *k, *qo, *ko, _stream(stream)))
+    dev = _device()
+    T, nq, d = qs = Q.shape
+    ks = (T, K.shape[1], d)
+    _check(load().qk_norm_rope_fwd(T, nq, ks[1], d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev),
+                                   *_rows("Q", Q, qs, dev), *_rows("K", K, ks, dev), *_rows("Qo", Qo, qs, dev),
+                                   *_rows("Ko", Ko, ks, dev), _here(dev, stream)))
 
 
 def qk_norm_rope_bwd(Q, K, dQo, dKo, dQ, dK, pos, inv_freq, wq=None, wk=None, dwq=None, dwk=None, ws=None, eps=1e-6,
                      rot=None, sections=None, interleaved=False, accumulate=True, stream=None):
     """Gradients dQ, dK of qk_norm_rope_fwd from dQo, dKo, and with the norm dwq, dwk [d] fp32 (ws: fp32 workspace of
     qk_norm_rope_workspace(d) floats).  Without the norm Q and K may be None."""
-    T, nq, d = dQo.shape
-    nk = dKo.shape[1]
-    g = [_rows(n, x, T, heads, d) for n, x, heads in (("dQo", dQo, nq), ("dKo", dKo, nk), ("dQ", dQ, nq), ("dK", dK, nk))]
-    x = [(None, 0), (None, 0)]
-    if wq is not None:
-        x = [_rows("Q", Q, T, nq, d), _rows("K", K, T, nk, d)]
-    _check(load().qk_norm_rope_bwd(T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps),
-                                   int(accumulate), *x[0], *x[1], *g[0], *g[1], *g[2], *g[3],
-                                   *_dw_args(d, wq, dwq, dwk, ws), _stream(stream)))
-
-
-def _dw_args(d, wq, dwq, dwk, ws):
-    if wq is None:
-        return None, None, None
-    f32 = torch.float32
-    return (_arg("dwq", dwq, f32, (d,)), _arg("dwk", dwk, f32, (d,)), _arg("ws", ws, f32, (qk_norm_rope_workspace(d),)))
+    dev = _device()
+    T, nq, d = qs = dQo.shape
+    ks = (T, dKo.shape[1], d)
+    norm = wq is not None
+    _check(load().qk_norm_rope_bwd(T, nq, ks[1], d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev),
+                                   int(accumulate), *(_rows("Q", Q, qs, dev) if norm else (None, 0)),
+                                   *(_rows("K", K, ks, dev) if norm else (None, 0)), *_rows("dQo", dQo, qs, dev),
+                                   *_rows("dKo", dKo, ks, dev), *_rows("dQ", dQ, qs, dev), *_rows("dK", dK, ks, dev),
+                                   *_dw_args(d, wq, dwq, dwk, ws, dev), _here(dev, stream)))
 
 
 class Rope:
@@ -301,33 +320,44 @@ class Rope:
             self.dwq, self.dwk = torch.zeros(d, **f32), torch.zeros(d, **f32)
             self.ws = torch.empty(qk_norm_rope_workspace(d), **f32)
 
-    def args(self, tokens):
+    def args(self, tokens, dev):
         return _rope_args(tokens, self.d, self.pos, self.inv_freq, self.wq, self.wk, self.rot, self.sections,
-                          self.interleaved, self.eps)
+                          self.interleaved, self.eps, dev)
 
 
 def attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, X, Wqkv, bqkv, Wo, bo, R, QKV, QKr, S, P, O,
                   out, stream=None):
     """attn_fwd with the norms and rotation of ``rope`` (a Rope) on its queries and keys; QKr [tokens, 2h] holds them."""
-    bf = torch.bfloat16
+    dev, rows = _device(), (tokens, h)
     pshape = (tokens // seq_len, nh, seq_len, seq_len)
-    _check(load().attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens),
-                                _arg("X", X, bf, (tokens, h)), _arg("Wqkv", Wqkv, bf, (h, 3 * h)),
-                                _arg("bqkv", bqkv, bf, (3 * h,)), _arg("Wo", Wo, bf, (h, h)), _arg("bo", bo, bf, (h,)),
-                                _arg("R", R, bf, (tokens, h), True), _arg("QKV", QKV, bf, (tokens, 3 * h)),
-                                _arg("QKr", QKr, bf, (tokens, 2 * h)), _arg("S", S, torch.float32, pshape),
-                                _arg("P", P, bf, pshape), _arg("O", O, bf, (tokens, h)),
-                                _arg("out", out, bf, (tokens, h)), _stream(stream)))
+    _check(load().attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens, dev),
+                                _arg("X", X, _bf16, rows, dev), _arg("Wqkv", Wqkv, _bf16, (h, 3 * h), dev),
+                                _arg("bqkv", bqkv, _bf16, (3 * h,), dev), _arg("Wo", Wo, _bf16, (h, h), dev),
+                                _arg("bo", bo, _bf16, (h,), dev), _opt("R", R, _bf16, rows, dev),
+                                _arg("QKV", QKV, _bf16, (tokens, 3 * h), dev), _arg("QKr", QKr, _bf16, (tokens, 2 * h), dev),
+                                _arg("S", S, _float, pshape, dev), _arg("P", P, _bf16, pshape, dev),
+                                _arg("O", O, _bf16, rows, dev), _arg("out", out, _bf16, rows, dev), _here(dev, stream)))
 
 
 def attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, residual_grad, accumulate, dOut, X, Wqkv, Wo,
                   QKV, QKr, P, O, dZ, dO, dP, dS, dQKV, dX, dWqkv, dbqkv, dWo, dbo, stream=None):
-    """attn_bwd of attn_rope_fwd; rope.dwq and rope.dwk receive the norm weights' gradients."""
-    _check(load().attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens),
-                                int(residual_grad), int(accumulate), _ptr(dOut), _ptr(X), _ptr(Wqkv), _ptr(Wo), _ptr(QKV),
-                                _arg("QKr", QKr, torch.bfloat16, (tokens, 2 * h)), _ptr(P), _ptr(O), _ptr(dZ), _ptr(dO),
-                                _ptr(dP), _ptr(dS), _ptr(dQKV), _ptr(dX), _ptr(dWqkv), _ptr(dbqkv), _ptr(dWo), _ptr(dbo),
-                                *_dw_args(rope.d, rope.wq, rope.dwq, rope.dwk, rope.ws), _stream(stream)))
+    """attn_bwd of attn_rope_fwd; rope.dwq and rope.dwk receive the norm weights' gradients.  dP: fp32, at least
+    n_seq * nh * seq_len floats."""
+    dev, rows = _device(), (tokens, h)
+    pshape = (tokens // seq_len, nh, seq_len, seq_len)
+    if dP is None or dP.dtype is not _float or dP.numel() < tokens * nh or dP.get_device() != dev or not dP.is_contiguous():
+        raise ValueError(f"dP must hold at least {tokens * nh} contiguous fp32 on the current device")
+    _check(load().attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens, dev),
+                                int(residual_grad), int(accumulate), _arg("dOut", dOut, _bf16, rows, dev),
+                                _arg("X", X, _bf16, rows, dev), _arg("Wqkv", Wqkv, _bf16, (h, 3 * h), dev),
+                                _arg("Wo", Wo, _bf16, (h, h), dev), _arg("QKV", QKV, _bf16, (tokens, 3 * h), dev),
+                                _arg("QKr", QKr, _bf16, (tokens, 2 * h), dev), _arg("P", P, _bf16, pshape, dev),
+                                _arg("O", O, _bf16, rows, dev), _arg("dZ", dZ, _bf16, rows, dev),
+                                _arg("dO", dO, _bf16, rows, dev), dP.data_ptr(), _arg("dS", dS, _bf16, pshape, dev),
+                                _arg("dQKV", dQKV, _bf16, (tokens, 3 * h), dev), _arg("dX", dX, _bf16, rows, dev),
+                                _arg("dWqkv", dWqkv, _float, (h, 3 * h), dev), _arg("dbqkv", dbqkv, _float, (3 * h,), dev),
+                                _arg("dWo", dWo, _float, (h, h), dev), _arg("dbo", dbo, _float, (h,), dev),
+                                *_dw_args(rope.d, rope.wq, rope.dwq, rope.dwk, rope.ws, dev), _here(dev, stream)))
 
 
 class AttnBuffers:
