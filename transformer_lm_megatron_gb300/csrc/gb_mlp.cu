@@ -29,6 +29,7 @@
 #include "attention.cuh"
 #include "attn_fused.cuh"
 #include "elementwise.cuh"
+#include "few_tokens.cuh"
 #include "gb_mlp.h"
 #include "gemm_tc.cuh"
 #include "qk_rope.cuh"
@@ -117,6 +118,7 @@ struct DeviceState {
   bool gemm_attr[96] = {};  // per GEMM instantiation: dynamic smem attribute set
   bool fa_attr = false;     // fused attention core: dynamic smem attribute set
   bool fb_attr = false;     // fused attention backward core: dynamic smem attribute set
+  bool few_attr[2] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
@@ -330,6 +332,7 @@ int launch_transposes(cudaStream_t s, int64_t rows, int cols, TransposeJob j0, T
   return launch_check(e, what);
 }
 
+#include "few_tokens_host.cuh"
 #include "qk_rope_host.cuh"
 
 template <int CHUNKS>
@@ -1118,6 +1121,25 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int T = (int)tokens;
   if (R == nullptr) R = X;
+  if (T <= kFewTokens) {
+    FewTokensParams f{};
+    f.T = T;
+    f.N = ffn;
+    f.K = h;
+    f.act = act;
+    f.bias = a;
+    f.GU = GU;
+    f.out = Y;
+    rc = launch_few_tokens<true>(st, A, X, f, s, kTraceGlu);
+    if (rc) return rc;
+    f.N = h;
+    f.K = ffn;
+    f.bias = b;
+    f.R = R;
+    f.out = O;
+    f.drop = make_dropout(p, seed, token_offset, h);
+    return launch_few_tokens<false>(st, B, Y, f, s, kTraceGluOut);
+  }
   rc = gemm_glu(st, X, A, a, GU, Y, T, ffn, h, act, s);
   if (rc) return rc;
   // O = R + dropout(Y B + b)
