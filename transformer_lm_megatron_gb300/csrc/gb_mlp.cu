@@ -1150,7 +1150,8 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   e.bias = b;
   e.out0 = O;
   e.drop = make_dropout(p, seed, token_offset, h);
-  return gemm(st, Y, false, ffn, B, true, h, T, h, ffn, e, s, kTraceGluOut, false, false);
+  return gemm(st, Y, false, ffn, B, true, h, T, h, ffn, e, s, kTraceGluOut, false, false,
+              few_waves(st, T, h));
 }
 
 int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
@@ -1187,7 +1188,8 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
   e.ld = h;
   e.in0 = residual_grad ? dO : nullptr;
   e.out0 = dX;
-  return gemm(st, dGU, false, 2 * (int64_t)ffn, A, false, 2 * (int64_t)ffn, T, h, 2 * ffn, e, s, kTraceGluDX, false, false);
+  return gemm(st, dGU, false, 2 * (int64_t)ffn, A, false, 2 * (int64_t)ffn, T, h, 2 * ffn, e, s, kTraceGluDX, false, false,
+              few_waves(st, T, h));
 }
 
 int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const mlp_bf16* X, const mlp_bf16* dZ,
@@ -1232,14 +1234,14 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   ea.ld = f2;
   ea.g_out = dA;
   rc = Xt ? gemm(st, Xt, false, T, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false)
-          : gemm(st, X, true, h, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false);
+          : gemm(st, X, true, h, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false, few_waves(st, h, f2));
   if (rc) return rc;
   EpiParams eb{};
   eb.kind = acc ? kEpiF32Add : kEpiF32Store;
   eb.ld = h;
   eb.g_out = dB;
   return dZt ? gemm(st, Y, true, ffn, dZt, false, T, ffn, h, T, eb, s, kTraceGluDW, false, false)
-             : gemm(st, Y, true, ffn, dZ, true, h, ffn, h, T, eb, s, kTraceGluDW, false, false);
+             : gemm(st, Y, true, ffn, dZ, true, h, ffn, h, T, eb, s, kTraceGluDW, false, false, few_waves(st, ffn, h));
 }
 
 int mlp_sync_status(void* stream) {

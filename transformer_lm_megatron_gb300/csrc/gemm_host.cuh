@@ -192,7 +192,7 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
 // never the first kernel of a call.
 int gemm(DeviceState* st, const void* a, bool a_mn, int64_t lda, const void* b, bool b_mn, int64_t ldb, int M, int N,
          int K, const EpiParams& ep, cudaStream_t stream, int trace_kind, bool late_wait = false,
-         bool static_ws = true) {
+         bool static_ws = true, bool few_waves = false) {
   const int mode = g_pair_mode.load(std::memory_order_relaxed);
   const bool pair = mode == 1 || (mode < 0 && M > kBM);
   CUtensorMap mA, mB, mC, mO0, mO1;
@@ -236,7 +236,9 @@ int gemm(DeviceState* st, const void* a, bool a_mn, int64_t lda, const void* b, 
   }
   const int l2_hints = g_l2_hints.load(std::memory_order_relaxed);
   // Reductions under 16 k-blocks leave the time in the epilogue: 8 epilogue warps.
-  const bool wide = (K + kBK - 1) / kBK < 16;
+  // few_waves (the gated block's launches): there is little of a next tile's main loop
+  // to hide the epilogue behind.
+  const bool wide = (K + kBK - 1) / kBK < 16 || few_waves;
 #define GB_LAUNCH(AM_, BM_)                                                                                        \
   (pair ? (wide ? launch_gemm_t<AM_, BM_, true, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast,   \
                                                              group, l2_hints, stream, trace_kind, 1, 1, kCausalNone, \
@@ -280,6 +282,13 @@ int make_half_map(CUtensorMap* m, const uint16_t* base, int64_t half_cols, int64
   return MLP_OK;
 }
 
+// Whether a GEMM of the gated block is of two waves of tiles or less, where 8 epilogue
+// warps pay (1317 tokens, h 1032, ffn 2744 forward: 54 us with 4, 49 us with 8; 2048
+// tokens, h 4096, ffn 16384: 486 and 498 us).  `cols` counts the MMA's columns.
+bool few_waves(const DeviceState* st, int M, int64_t cols) {
+  return (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
+}
+
 // G, U = X A + a and Y = act(G) U in one launch.  A [h, 2 ffn], bias a [2 ffn] or null;
 // GU [T, 2 ffn] may be null.
 int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16_t* a, uint16_t* GU, uint16_t* Y, int T,
@@ -303,7 +312,7 @@ int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16
   e.bias = a;
   e.act = act;
   const int raster_n_fast = T > 2 * (int64_t)ffn ? 1 : 0;
-  const bool wide = (h + kBK - 1) / kBK < 16;
+  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, 2 * (int64_t)ffn);
 #define GB_GLU(PAIR_, WIDE_)                                                                                          \
   launch_gemm_t<false, true, PAIR_, false, WIDE_, kGatedFwd>(st, mA, mB, mC, mGU, mY, T, ffn, h, e, raster_n_fast, 0, 0, \
                                                              stream, kTraceGlu, 1, 1, kCausalNone, false, false)
@@ -330,7 +339,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
   e.in0 = GU;
   e.act = act;
   const int raster_n_fast = T > ffn ? 1 : 0;
-  const bool wide = (h + kBK - 1) / kBK < 16;
+  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, ffn);
 #define GB_DGLU(PAIR_, WIDE_)                                                                                         \
   launch_gemm_t<false, false, PAIR_, false, WIDE_, kGatedBwd>(st, mA, mB, mC, mOut, mIn, T, ffn, h, e, raster_n_fast, 0, \
                                                               0, stream, kTraceDGlu, 1, 1, kCausalNone, false, false)
