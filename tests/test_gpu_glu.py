@@ -163,6 +163,9 @@ SHAPES = [
     (200, 320, 1000, "silu", 0.1, True),
     (257, 1032, 2744, "gelu", 0.1, True),
     (640, 2056, 328, "silu", 0.0, True),
+    (1100, 264, 520, "gelu", 0.1, True),     # weight gradients of few tiles and a long reduction
+    (1610, 136, 264, "silu", 0.0, True),
+    (385, 3080, 264, "gelu", 0.1, False),
 ]
 
 

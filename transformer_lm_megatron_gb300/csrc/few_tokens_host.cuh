@@ -2,8 +2,13 @@
 // Included by gb_mlp.cu inside its anonymous namespace.
 #pragma once
 
-// Up to this many tokens the forward takes the few-token launches.
-constexpr int kFewTokens = 128;
+// Up to this many tokens the forward's two products take the few-token launches, beyond
+// them the GEMMs with shared-out reductions.  Measured, few-token / GEMM (us, both products):
+// G, U and the gate: 48 tokens at h 4096, ffn 16384 69 / 75, 96 tokens 79 / 80, 160 tokens
+// 124 / 96; h 2048, ffn 5464 27 / 34, 36 / 39, 46 / 39.  O: 48 tokens 69 / 76 and 27 / 29,
+// 96 tokens 80 / 82 and 36 / 35, 160 tokens 96 / 93 and 39 / 35.
+constexpr int kFewTokensGates = 128;
+constexpr int kFewTokensOut = 64;
 
 template <bool GATED>
 int launch_few_tokens(DeviceState* st, const uint16_t* W, const uint16_t* X, FewTokensParams p, cudaStream_t s,

@@ -31,6 +31,7 @@
 #include "elementwise.cuh"
 #include "few_tokens.cuh"
 #include "gb_mlp.h"
+#include "gemm_split.cuh"
 #include "gemm_tc.cuh"
 #include "qk_rope.cuh"
 
@@ -118,6 +119,7 @@ struct DeviceState {
   bool gemm_attr[96] = {};  // per GEMM instantiation: dynamic smem attribute set
   bool fa_attr = false;     // fused attention core: dynamic smem attribute set
   bool fb_attr = false;     // fused attention backward core: dynamic smem attribute set
+  int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 1) CTAs; [0]: set up
   bool few_attr[2] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
@@ -226,6 +228,8 @@ cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block, size_t
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+int launch_check(cudaError_t e, const char* what);
 
 #include "gemm_host.cuh"
 
@@ -1121,9 +1125,9 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int T = (int)tokens;
   if (R == nullptr) R = X;
-  if (T <= kFewTokens) {
-    FewTokensParams f{};
-    f.T = T;
+  FewTokensParams f{};
+  f.T = T;
+  if (T <= kFewTokensGates) {
     f.N = ffn;
     f.K = h;
     f.act = act;
@@ -1131,17 +1135,20 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
     f.GU = GU;
     f.out = Y;
     rc = launch_few_tokens<true>(st, A, X, f, s, kTraceGlu);
-    if (rc) return rc;
+  } else {
+    rc = gemm_glu(st, X, A, a, GU, Y, T, ffn, h, act, s);
+  }
+  if (rc) return rc;
+  const DropoutParams drop = make_dropout(p, seed, token_offset, h);
+  if (T <= kFewTokensOut) {
     f.N = h;
     f.K = ffn;
     f.bias = b;
     f.R = R;
     f.out = O;
-    f.drop = make_dropout(p, seed, token_offset, h);
+    f.drop = drop;
     return launch_few_tokens<false>(st, B, Y, f, s, kTraceGluOut);
   }
-  rc = gemm_glu(st, X, A, a, GU, Y, T, ffn, h, act, s);
-  if (rc) return rc;
   // O = R + dropout(Y B + b)
   EpiParams e{};
   e.kind = kEpiDropRes;
@@ -1149,9 +1156,8 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   e.in0 = R;
   e.bias = b;
   e.out0 = O;
-  e.drop = make_dropout(p, seed, token_offset, h);
-  return gemm(st, Y, false, ffn, B, true, h, T, h, ffn, e, s, kTraceGluOut, false, false,
-              few_waves(st, T, h));
+  e.drop = drop;
+  return gemm_block<false, true>(st, Y, ffn, B, h, T, h, ffn, e, s, kTraceGluOut);
 }
 
 int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint64_t token_offset, int act,
@@ -1188,8 +1194,7 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
   e.ld = h;
   e.in0 = residual_grad ? dO : nullptr;
   e.out0 = dX;
-  return gemm(st, dGU, false, 2 * (int64_t)ffn, A, false, 2 * (int64_t)ffn, T, h, 2 * ffn, e, s, kTraceGluDX, false, false,
-              few_waves(st, T, h));
+  return gemm_block<false, false>(st, dGU, 2 * (int64_t)ffn, A, 2 * (int64_t)ffn, T, h, 2 * ffn, e, s, kTraceGluDX);
 }
 
 int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const mlp_bf16* X, const mlp_bf16* dZ,
@@ -1233,15 +1238,15 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   ea.kind = acc ? kEpiF32Add : kEpiF32Store;
   ea.ld = f2;
   ea.g_out = dA;
-  rc = Xt ? gemm(st, Xt, false, T, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false)
-          : gemm(st, X, true, h, dGU, true, f2, h, f2, T, ea, s, kTraceGluDW, false, false, few_waves(st, h, f2));
+  rc = Xt ? gemm_block<false, true>(st, Xt, T, dGU, f2, h, f2, T, ea, s, kTraceGluDW)
+          : gemm_block<true, true>(st, X, h, dGU, f2, h, f2, T, ea, s, kTraceGluDW);
   if (rc) return rc;
   EpiParams eb{};
   eb.kind = acc ? kEpiF32Add : kEpiF32Store;
   eb.ld = h;
   eb.g_out = dB;
-  return dZt ? gemm(st, Y, true, ffn, dZt, false, T, ffn, h, T, eb, s, kTraceGluDW, false, false)
-             : gemm(st, Y, true, ffn, dZ, true, h, ffn, h, T, eb, s, kTraceGluDW, false, false, few_waves(st, ffn, h));
+  return dZt ? gemm_block<true, false>(st, Y, ffn, dZt, T, ffn, h, T, eb, s, kTraceGluDW)
+             : gemm_block<true, true>(st, Y, ffn, dZ, h, ffn, h, T, eb, s, kTraceGluDW);
 }
 
 int mlp_sync_status(void* stream) {

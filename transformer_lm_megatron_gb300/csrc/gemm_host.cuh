@@ -289,6 +289,76 @@ bool few_waves(const DeviceState* st, int M, int64_t cols) {
   return (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
 }
 
+// The pairs to share one tile's reduction among (k_gemm_split), or 1 where the tiles fill
+// the SMs by themselves.  Each pair has 6 k-blocks or more, as many as its ring holds.
+template <bool AM, bool BM, int GATED>
+int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
+  *split = 1;
+  if (g_pair_mode.load(std::memory_order_relaxed) == 0) return MLP_OK;
+  auto kern = k_gemm_split<AM, BM, GATED>;
+  int* clusters = st->split_clusters[(AM ? 2 : 0) + (BM ? 1 : 0) + 4 * GATED];
+  if (clusters[0] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGsSmemBytes);
+    if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (split GEMM): %s", cudaGetErrorString(e));
+    for (int s = 2; s <= kGsMaxSplit; ++s) {
+      cudaLaunchConfig_t qc = {};
+      qc.gridDim = dim3(2 * (unsigned)s * st->sms);
+      qc.blockDim = dim3(kGsThreads);
+      qc.dynamicSmemBytes = kGsSmemBytes;
+      cudaLaunchAttribute qa[1];
+      qa[0].id = cudaLaunchAttributeClusterDimension;
+      qa[0].val.clusterDim.x = 2 * (unsigned)s;
+      qa[0].val.clusterDim.y = qa[0].val.clusterDim.z = 1;
+      qc.attrs = qa;
+      qc.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &qc) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      clusters[s - 1] = n;
+    }
+    clusters[0] = 1;
+  }
+  const int64_t tiles = (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN);
+  const int num_kb = (K + kBK - 1) / kBK;
+  for (int s = kGsMaxSplit; s >= 2; --s)
+    if (tiles <= clusters[s - 1] && num_kb >= kGsStages * s) {
+      *split = s;
+      break;
+    }
+  return MLP_OK;
+}
+
+template <bool AM, bool BM, int GATED>
+int launch_gemm_split(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB, int M, int N, int K,
+                      const EpiParams& ep, int split, cudaStream_t stream, int trace_kind) {
+  constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;
+  const int num_m = (M + 2 * kBM - 1) / (2 * kBM), tiles = num_m * ((N + kTileN - 1) / kTileN);
+  const int ts = trace_pre(stream);
+  const cudaError_t e =
+      launch_kernel(k_gemm_split<AM, BM, GATED>, dim3((unsigned)(tiles * 2 * split)), dim3(kGsThreads), kGsSmemBytes,
+                    stream, 2 * (unsigned)split, 1, mA, mB, M, N, K, ep, split, num_m, st->status);
+  trace_post(ts, stream, trace_kind, M, N, K);
+  return launch_check(e, "split GEMM");
+}
+
+// A plain GEMM of the gated block: its tiles' reductions shared out where they are few.
+template <bool AM, bool BM>
+int gemm_block(DeviceState* st, const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int M, int N, int K,
+               const EpiParams& ep, cudaStream_t stream, int trace_kind) {
+  int split = 1;
+  int rc = split_pairs<AM, BM, kGatedNone>(st, M, N, K, &split);
+  if (rc) return rc;
+  if (split == 1)  // ((MN, K) is not instantiated with 8 epilogue warps)
+    return gemm(st, a, AM, lda, b, BM, ldb, M, N, K, ep, stream, trace_kind, false, false, few_waves(st, M, N) && (!AM || BM));
+  CUtensorMap mA, mB;
+  rc = operand_map(&mA, a, AM, M, K, lda, kBM);
+  if (!rc) rc = operand_map(&mB, b, BM, N, K, ldb, GemmCfg<true>::kBLoadN);
+  if (rc) return rc;
+  return launch_gemm_split<AM, BM, kGatedNone>(st, mA, mB, M, N, K, ep, split, stream, trace_kind);
+}
+
 // G, U = X A + a and Y = act(G) U in one launch.  A [h, 2 ffn], bias a [2 ffn] or null;
 // GU [T, 2 ffn] may be null.
 int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16_t* a, uint16_t* GU, uint16_t* Y, int T,
@@ -311,6 +381,10 @@ int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16
   e.out1 = Y;
   e.bias = a;
   e.act = act;
+  int split = 1;
+  rc = split_pairs<false, true, kGatedFwd>(st, T, 2 * (int64_t)ffn, h, &split);
+  if (rc) return rc;
+  if (split > 1) return launch_gemm_split<false, true, kGatedFwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceGlu);
   const int raster_n_fast = T > 2 * (int64_t)ffn ? 1 : 0;
   const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, 2 * (int64_t)ffn);
 #define GB_GLU(PAIR_, WIDE_)                                                                                          \
@@ -325,10 +399,16 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
               int h, int act, cudaStream_t stream) {
   const int mode = g_pair_mode.load(std::memory_order_relaxed);
   const bool pair = mode == 1 || (mode < 0 && T > kBM);
+  int split = 1;
+  int rc = split_pairs<false, false, kGatedBwd>(st, T, ffn, h, &split);
+  if (rc) return rc;
   CUtensorMap mA, mB, mC, mOut, mIn;
   memset(&mC, 0, sizeof(mC));
-  int rc = operand_map(&mA, dZ, false, T, h, h, kBM);
-  if (!rc) rc = operand_map(&mB, B, false, ffn, h, h, pair ? GemmCfg<true>::kBLoadN : GemmCfg<false>::kBLoadN);
+  rc = operand_map(&mA, dZ, false, T, h, h, kBM);
+  // (a CTA of a pair loads half of a tile's columns, whichever kernel it runs)
+  if (!rc)
+    rc = operand_map(&mB, B, false, ffn, h, h,
+                     pair || split > 1 ? GemmCfg<true>::kBLoadN : GemmCfg<false>::kBLoadN);
   if (!rc)
     rc = make_half_map(&mOut, dGU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   if (!rc) rc = make_half_map(&mIn, GU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
@@ -338,6 +418,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
   e.out0 = dGU;
   e.in0 = GU;
   e.act = act;
+  if (split > 1) return launch_gemm_split<false, false, kGatedBwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceDGlu);
   const int raster_n_fast = T > ffn ? 1 : 0;
   const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, ffn);
 #define GB_DGLU(PAIR_, WIDE_)                                                                                         \
