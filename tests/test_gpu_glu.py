@@ -166,6 +166,10 @@ SHAPES = [
     (1100, 264, 520, "gelu", 0.1, True),     # weight gradients of few tiles and a long reduction
     (1610, 136, 264, "silu", 0.0, True),
     (385, 3080, 264, "gelu", 0.1, False),
+    # weights too large for the few-token launches: tiles of 256 x 256, shared out or not
+    (300, 2056, 6152, "silu", 0.1, True),
+    (1300, 2568, 1288, "gelu", 0.0, False),
+    (2100, 520, 4104, "silu", 0.1, True),
 ]
 
 
@@ -204,7 +208,8 @@ def test_forward_and_backward(T, h, ffn, act, p, bias):
 
 
 @pytest.mark.parametrize("cta_pair_mode", [0, 1], indirect=True, ids=["single", "pair"])
-@pytest.mark.parametrize("T,h,ffn,act", [(300, 264, 392, "gelu"), (300, 1096, 392, "silu"), (100, 1096, 392, "gelu")])
+@pytest.mark.parametrize("T,h,ffn,act", [(300, 264, 392, "gelu"), (300, 1096, 392, "silu"), (100, 1096, 392, "gelu"),
+                                          (700, 2568, 2056, "silu"), (530, 264, 136, "gelu")])
 def test_both_cta_modes(T, h, ffn, act, cta_pair_mode):
     c = Case(T, h, ffn, act)
     bf = dict(dtype=torch.bfloat16, device="cuda")

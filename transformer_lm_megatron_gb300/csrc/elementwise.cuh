@@ -123,17 +123,14 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// out[c] (+)= sum over rows of x[r * ld + c], c < cols.  Same grid and clusters.
-__global__ void __launch_bounds__(kColThreads)
-    k_colsum_bf16(const uint16_t* __restrict__ x, int64_t ld, float* __restrict__ out, int64_t rows, int cols,
-                  int accumulate) {
+// out[c] (+)= sum over rows of x[r * ld + c], c < cols, for column block `block`.
+__device__ __forceinline__ void colsum_block(const uint16_t* __restrict__ x, int64_t ld, float* __restrict__ out,
+                                             int64_t rows, int cols, int block, int accumulate) {
   __shared__ float part[kColRowLanes][kColsPerCta + 1];
   __shared__ float psum[kColsPerCta];
-  grid_dependency_wait();
-  grid_launch_dependents();
   const int cg = threadIdx.x & 7;
   const int rl = threadIdx.x >> 3;
-  const int col = blockIdx.x * kColsPerCta + cg * 8;
+  const int col = block * kColsPerCta + cg * 8;
   const int64_t r_begin = rows * (int64_t)blockIdx.y / gridDim.y;
   const int64_t r_end = rows * (int64_t)(blockIdx.y + 1) / gridDim.y;
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -160,9 +157,33 @@ __global__ void __launch_bounds__(kColThreads)
   __syncthreads();
   const float tot = cluster_colsum(part, psum);
   if (blockIdx.y == 0 && threadIdx.x < kColsPerCta) {
-    const int c = blockIdx.x * kColsPerCta + threadIdx.x;
+    const int c = block * kColsPerCta + threadIdx.x;
     if (c < cols) out[c] = accumulate ? out[c] + tot : tot;
   }
+}
+
+// The column sums of one matrix.  Same grid and clusters.
+__global__ void __launch_bounds__(kColThreads)
+    k_colsum_bf16(const uint16_t* __restrict__ x, int64_t ld, float* __restrict__ out, int64_t rows, int cols,
+                  int accumulate) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  colsum_block(x, ld, out, rows, cols, blockIdx.x, accumulate);
+}
+
+// The column sums of two contiguous matrices of as many rows, the gated block's da and db
+// in one launch (two launches took 14 us of 51 at 1317 tokens, h 1032, ffn 2744).  Either
+// may have no columns.  Grid (blocks of x0 + blocks of x1, split), clusters as above.
+__global__ void __launch_bounds__(kColThreads)
+    k_colsum_two(const uint16_t* x0, float* out0, int cols0, const uint16_t* x1, float* out1, int cols1, int64_t rows,
+                 int accumulate) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int blocks0 = (cols0 + kColsPerCta - 1) / kColsPerCta;
+  const bool second = (int)blockIdx.x >= blocks0;
+  const int cols = second ? cols1 : cols0;
+  colsum_block(second ? x1 : x0, cols, second ? out1 : out0, rows, cols, (int)blockIdx.x - (second ? blocks0 : 0),
+               accumulate);
 }
 
 // p[0 .. n) = 0 with 16-byte stores; n % 4 == 0 and p 16-byte aligned.

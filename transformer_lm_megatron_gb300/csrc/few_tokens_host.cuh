@@ -2,44 +2,70 @@
 // Included by gb_mlp.cu inside its anonymous namespace.
 #pragma once
 
-// Up to this many tokens the forward's two products take the few-token launches, beyond
-// them the GEMMs with shared-out reductions.  Measured, few-token / GEMM (us, both products):
-// G, U and the gate: 48 tokens at h 4096, ffn 16384 69 / 75, 96 tokens 79 / 80, 160 tokens
-// 124 / 96; h 2048, ffn 5464 27 / 34, 36 / 39, 46 / 39.  O: 48 tokens 69 / 76 and 27 / 29,
-// 96 tokens 80 / 82 and 36 / 35, 160 tokens 96 / 93 and 39 / 35.
-constexpr int kFewTokensGates = 128;
-constexpr int kFewTokensOut = 64;
+// Shared memory of a CTA: half of an SM's.
+constexpr int kFtSmem = 110 * 1024;
 
-template <bool GATED>
+// Whether a product of the gated block over `weight_bytes` of weights takes the few-token
+// launch rather than the GEMMs of 256 x 256 tiles: where its tokens fit one tile of 64, and
+// beyond while the weights, read from L2 once for each 64 tokens, stay under a limit: for a
+// pass's first product (G, U and the gate, or dG and dU) of up to 512 tokens 64 MB, for its
+// second (O, or dX) 96 MB.  Measured, few-token / GEMM (us of a pass, the other product alike):
+//   both   48 tokens, h 4096, ffn 16384 68 / 79; h 2048, ffn 5464 21 / 36
+//   first  200 tokens, h 1024, ffn 4096 19 / 22; 192 tokens, h 2048, ffn 5464 34 / 31; 1600
+//          tokens, h 640, ffn 1280 25 / 21; backward: 256 tokens, h 1024, ffn 4096 23 / 28, h
+//          376, ffn 4752 19 / 23; 1024 tokens, h 376, ffn 4752 49 / 39
+//   second 400 tokens, h 1024, ffn 4096 25 / 30; 192 tokens, h 4096, ffn 16384 108 / 91; 1600
+//          tokens, h 1032, ffn 2744 55 / 47; backward: 128 tokens, h 2048, ffn 5464 29 / 38;
+//          512 tokens, h 376, ffn 4752 25 / 34; 1024 tokens, h 1024, ffn 4096 55 / 42
+bool few_tokens_first(int T, int64_t weight_bytes) {
+  return T <= 64 || (T <= 512 && (T + 63) / 64 * weight_bytes <= 64ll << 20);
+}
+bool few_tokens_second(int T, int64_t weight_bytes) {
+  return T <= 64 || (T + 63) / 64 * weight_bytes <= 96ll << 20;
+}
+
+template <int KIND>
 int launch_few_tokens(DeviceState* st, const uint16_t* W, const uint16_t* X, FewTokensParams p, cudaStream_t s,
                       int trace_kind) {
+  constexpr bool GATED = KIND == kFtGates, W_MN = KIND == kFtGates || KIND == kFtOut;
   p.tpad = 16;
   while (p.tpad < p.T && p.tpad < kFtMaxTokens) p.tpad *= 2;
   const int tiles = (p.N + (GATED ? 64 : 128) - 1) / (GATED ? 64 : 128), num_kb = (p.K + kBK - 1) / kBK;
   const int token_tiles = (p.T + p.tpad - 1) / p.tpad;
-  // A stage is 16 KB of weights and 128 bytes a token; two CTAs to an SM share its 227 KB.
-  const int stage_bytes = (int)kFtWBytes + p.tpad * kBK * 2;
-  p.stages = (int)(110 * 1024 / stage_bytes);
-  if (p.stages > kFtMaxStages) p.stages = kFtMaxStages;
-  const int smem = p.stages * stage_bytes + 1024;
-  // CTAs share a tile's reduction until two to an SM are at work, each with 4 k-blocks or more.
+  // CTAs share a tile's reduction until two to an SM are at work, each with 4 k-blocks or
+  // more.  A stage is 16 KB of weights and 128 bytes a token; two CTAs share an SM's 227 KB,
+  // with three stages each or more beside what they are sent (a CTA by itself leaves its
+  // sums in its own ring).  27 tokens at h 2048, ffn 5464: 19 us; with CTAs for 1.25 or 1.5
+  // to an SM 20 us, with three small CTAs to an SM 32 us (two stages each).
+  const int rows = p.T < p.tpad ? p.T : p.tpad, stage_bytes = (int)kFtWBytes + p.tpad * kBK * 2;
   int64_t split = 2 * (int64_t)st->sms / ((int64_t)tiles * token_tiles);
   if (split > num_kb / 4) split = num_kb / 4;
   p.split = split < 1 ? 1 : split > kFtMaxSplit ? kFtMaxSplit : (int)split;
+  int sent_bytes;
+  for (;; --p.split) {
+    p.per_log2 = 0;
+    while ((p.split << p.per_log2) < rows) ++p.per_log2;
+    sent_bytes = p.split > 1 ? (p.split << p.per_log2) * kFtTileW * 4 : 0;
+    p.stages = (kFtSmem - sent_bytes) / stage_bytes;
+    if (p.split == 1 || p.stages >= 3) break;
+  }
+  if (p.stages > kFtMaxStages) p.stages = kFtMaxStages;
+  const int smem = p.stages * stage_bytes + sent_bytes + 1024;
   CUtensorMap mW, mX;
   int rc = GATED ? make_half_map(&mW, W, p.N, p.K, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
-                 : make_map(&mW, W, p.N, p.K, p.N, 64, kBK);
+           : W_MN ? make_map(&mW, W, p.N, p.K, p.N, 64, kBK)
+                  : make_map(&mW, W, p.K, p.N, p.K, kBK, kFtTileW);
   if (!rc) rc = make_map(&mX, X, p.K, p.T, p.K, kBK, (uint32_t)p.tpad);
   if (rc) return rc;
-  auto kern = k_few_tokens<GATED>;
-  bool& ready = st->few_attr[GATED ? 1 : 0];
+  auto kern = k_few_tokens<KIND>;
+  bool& ready = st->few_attr[KIND];
   if (!ready) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 111 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFtSmem + 1024);
     if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (few tokens): %s", cudaGetErrorString(e));
     ready = true;
   }
   const int ts = trace_pre(s);
-  const cudaError_t e = launch_kernel(kern, dim3((unsigned)(tiles * p.split), (unsigned)token_tiles), dim3(kFtThreads),
+  const cudaError_t e = launch_kernel(kern, dim3((unsigned)(tiles * token_tiles * p.split)), dim3(kFtThreads),
                                       (size_t)smem, s, (unsigned)p.split, 1, mW, mX, p, st->status);
   trace_post(ts, s, trace_kind, p.T, p.N, p.K);
   return launch_check(e, "few-token product");

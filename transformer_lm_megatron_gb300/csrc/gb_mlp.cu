@@ -120,7 +120,7 @@ struct DeviceState {
   bool fa_attr = false;     // fused attention core: dynamic smem attribute set
   bool fb_attr = false;     // fused attention backward core: dynamic smem attribute set
   int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 1) CTAs; [0]: set up
-  bool few_attr[2] = {};    // few-token products: dynamic smem attribute set
+  bool few_attr[4] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
@@ -1127,27 +1127,27 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   if (R == nullptr) R = X;
   FewTokensParams f{};
   f.T = T;
-  if (T <= kFewTokensGates) {
+  if (few_tokens_first(T, 4ll * h * ffn)) {
     f.N = ffn;
     f.K = h;
     f.act = act;
     f.bias = a;
     f.GU = GU;
     f.out = Y;
-    rc = launch_few_tokens<true>(st, A, X, f, s, kTraceGlu);
+    rc = launch_few_tokens<kFtGates>(st, A, X, f, s, kTraceGlu);
   } else {
     rc = gemm_glu(st, X, A, a, GU, Y, T, ffn, h, act, s);
   }
   if (rc) return rc;
   const DropoutParams drop = make_dropout(p, seed, token_offset, h);
-  if (T <= kFewTokensOut) {
+  if (few_tokens_second(T, 2ll * h * ffn)) {
     f.N = h;
     f.K = ffn;
     f.bias = b;
-    f.R = R;
+    f.in = R;
     f.out = O;
     f.drop = drop;
-    return launch_few_tokens<false>(st, B, Y, f, s, kTraceGluOut);
+    return launch_few_tokens<kFtOut>(st, B, Y, f, s, kTraceGluOut);
   }
   // O = R + dropout(Y B + b)
   EpiParams e{};
@@ -1186,8 +1186,26 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
     if (rc) return rc;
     g = dZ;
   }
-  rc = gemm_dglu(st, g, B, GU, dGU, T, ffn, h, act, s);
+  FewTokensParams f{};
+  f.T = T;
+  if (few_tokens_first(T, 2ll * h * ffn)) {
+    f.N = ffn;
+    f.K = h;
+    f.act = act;
+    f.in = GU;
+    f.out = dGU;
+    rc = launch_few_tokens<kFtDGates>(st, B, g, f, s, kTraceDGlu);
+  } else {
+    rc = gemm_dglu(st, g, B, GU, dGU, T, ffn, h, act, s);
+  }
   if (rc) return rc;
+  if (few_tokens_second(T, 4ll * h * ffn)) {
+    f.N = h;
+    f.K = 2 * ffn;
+    f.in = residual_grad ? dO : nullptr;
+    f.out = dX;
+    return launch_few_tokens<kFtDX>(st, A, dGU, f, s, kTraceGluDX);
+  }
   // dX = [dO +] dGU A^T: the reduction runs over both halves
   EpiParams e{};
   e.kind = kEpiResAdd;
@@ -1212,17 +1230,20 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int T = (int)tokens, f2 = 2 * ffn, acc = accumulate ? 1 : 0;
-  auto colsum = [&](const mlp_bf16* x, int cols, float* out) {
+  // da and db; the products read nothing that this launch writes, so they need not wait
+  // for its end (late wait), and dB's need not wait for dA's
+  const bool sums = da != nullptr || db != nullptr;
+  if (sums) {
+    const int c0 = da != nullptr ? f2 : 0, c1 = db != nullptr ? h : 0;
+    const int blocks = (c0 + kColsPerCta - 1) / kColsPerCta + (c1 + kColsPerCta - 1) / kColsPerCta;
+    const unsigned split = colsum_split(st, (int64_t)blocks * kColsPerCta, k_colsum_two);
     const int ts = trace_pre(s);
-    const unsigned split = colsum_split(st, cols, k_colsum_bf16);
-    const cudaError_t e =
-        launch_kernel(k_colsum_bf16, dim3((cols + kColsPerCta - 1) / kColsPerCta, split), dim3(kColThreads), 0, s, 1,
-                      split, (const uint16_t*)x, (int64_t)cols, out, tokens, cols, acc);
-    trace_post(ts, s, kTraceColsum, tokens, cols, 0);
-    return launch_check(e, "bias-gradient column sum");
-  };
-  if (da != nullptr && (rc = colsum(dGU, f2, da))) return rc;
-  if (db != nullptr && (rc = colsum(dZ, h, db))) return rc;
+    const cudaError_t e = launch_kernel(k_colsum_two, dim3((unsigned)blocks, split), dim3(kColThreads), 0, s, 1, split, dGU,
+                                        da, c0, dZ, db, c1, tokens, acc);
+    trace_post(ts, s, kTraceColsum, tokens, c0 + c1, 0);
+    rc = launch_check(e, "bias-gradient column sums");
+    if (rc) return rc;
+  }
   // transposed copies of X and dZ for large products, as in mlp_bwd
   const mlp_bf16* Xt = nullptr;
   const mlp_bf16* dZt = nullptr;
@@ -1239,14 +1260,14 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   ea.ld = f2;
   ea.g_out = dA;
   rc = Xt ? gemm_block<false, true>(st, Xt, T, dGU, f2, h, f2, T, ea, s, kTraceGluDW)
-          : gemm_block<true, true>(st, X, h, dGU, f2, h, f2, T, ea, s, kTraceGluDW);
+          : gemm_block<true, true>(st, X, h, dGU, f2, h, f2, T, ea, s, kTraceGluDW, sums);
   if (rc) return rc;
   EpiParams eb{};
   eb.kind = acc ? kEpiF32Add : kEpiF32Store;
   eb.ld = h;
   eb.g_out = dB;
   return dZt ? gemm_block<true, false>(st, Y, ffn, dZt, T, ffn, h, T, eb, s, kTraceGluDW)
-             : gemm_block<true, true>(st, Y, ffn, dZ, h, ffn, h, T, eb, s, kTraceGluDW);
+             : gemm_block<true, true>(st, Y, ffn, dZ, h, ffn, h, T, eb, s, kTraceGluDW, true);
 }
 
 int mlp_sync_status(void* stream) {

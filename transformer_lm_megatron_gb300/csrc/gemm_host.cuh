@@ -282,11 +282,12 @@ int make_half_map(CUtensorMap* m, const uint16_t* base, int64_t half_cols, int64
   return MLP_OK;
 }
 
-// Whether a GEMM of the gated block is of two waves of tiles or less, where 8 epilogue
-// warps pay (1317 tokens, h 1032, ffn 2744 forward: 54 us with 4, 49 us with 8; 2048
-// tokens, h 4096, ffn 16384: 486 and 498 us).  `cols` counts the MMA's columns.
-bool few_waves(const DeviceState* st, int M, int64_t cols) {
-  return (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
+// Whether a GEMM of the gated block is of two waves of tiles or less of under 64 k-blocks
+// each, where 8 epilogue warps pay (1317 tokens, h 1032, ffn 2744 forward: 54 us with 4, 49
+// us with 8; 2048 tokens, h 4096, ffn 16384, with 256 k-blocks: 486 and 498 us).  `cols`
+// counts the MMA's columns.
+bool few_waves(const DeviceState* st, int M, int64_t cols, int K) {
+  return (K + kBK - 1) / kBK < 64 && (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
 }
 
 // The pairs to share one tile's reduction among (k_gemm_split), or 1 where the tiles fill
@@ -332,13 +333,14 @@ int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
 
 template <bool AM, bool BM, int GATED>
 int launch_gemm_split(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB, int M, int N, int K,
-                      const EpiParams& ep, int split, cudaStream_t stream, int trace_kind) {
+                      const EpiParams& ep, int split, cudaStream_t stream, int trace_kind, bool late_wait = false) {
   constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;
   const int num_m = (M + 2 * kBM - 1) / (2 * kBM), tiles = num_m * ((N + kTileN - 1) / kTileN);
   const int ts = trace_pre(stream);
   const cudaError_t e =
       launch_kernel(k_gemm_split<AM, BM, GATED>, dim3((unsigned)(tiles * 2 * split)), dim3(kGsThreads), kGsSmemBytes,
-                    stream, 2 * (unsigned)split, 1, mA, mB, M, N, K, ep, split, num_m, st->status);
+                    stream, 2 * (unsigned)split, 1, mA, mB, M, N, K, ep, split, num_m,
+                    late_wait && g_late_wait.load(std::memory_order_relaxed) ? 1 : 0, st->status);
   trace_post(ts, stream, trace_kind, M, N, K);
   return launch_check(e, "split GEMM");
 }
@@ -346,17 +348,18 @@ int launch_gemm_split(DeviceState* st, const CUtensorMap& mA, const CUtensorMap&
 // A plain GEMM of the gated block: its tiles' reductions shared out where they are few.
 template <bool AM, bool BM>
 int gemm_block(DeviceState* st, const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int M, int N, int K,
-               const EpiParams& ep, cudaStream_t stream, int trace_kind) {
+               const EpiParams& ep, cudaStream_t stream, int trace_kind, bool late_wait = false) {
   int split = 1;
   int rc = split_pairs<AM, BM, kGatedNone>(st, M, N, K, &split);
   if (rc) return rc;
   if (split == 1)  // ((MN, K) is not instantiated with 8 epilogue warps)
-    return gemm(st, a, AM, lda, b, BM, ldb, M, N, K, ep, stream, trace_kind, false, false, few_waves(st, M, N) && (!AM || BM));
+    return gemm(st, a, AM, lda, b, BM, ldb, M, N, K, ep, stream, trace_kind, late_wait, false,
+                few_waves(st, M, N, K) && (!AM || BM));
   CUtensorMap mA, mB;
   rc = operand_map(&mA, a, AM, M, K, lda, kBM);
   if (!rc) rc = operand_map(&mB, b, BM, N, K, ldb, GemmCfg<true>::kBLoadN);
   if (rc) return rc;
-  return launch_gemm_split<AM, BM, kGatedNone>(st, mA, mB, M, N, K, ep, split, stream, trace_kind);
+  return launch_gemm_split<AM, BM, kGatedNone>(st, mA, mB, M, N, K, ep, split, stream, trace_kind, late_wait);
 }
 
 // G, U = X A + a and Y = act(G) U in one launch.  A [h, 2 ffn], bias a [2 ffn] or null;
@@ -386,7 +389,7 @@ int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16
   if (rc) return rc;
   if (split > 1) return launch_gemm_split<false, true, kGatedFwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceGlu);
   const int raster_n_fast = T > 2 * (int64_t)ffn ? 1 : 0;
-  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, 2 * (int64_t)ffn);
+  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, 2 * (int64_t)ffn, h);
 #define GB_GLU(PAIR_, WIDE_)                                                                                          \
   launch_gemm_t<false, true, PAIR_, false, WIDE_, kGatedFwd>(st, mA, mB, mC, mGU, mY, T, ffn, h, e, raster_n_fast, 0, 0, \
                                                              stream, kTraceGlu, 1, 1, kCausalNone, false, false)
@@ -420,7 +423,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
   e.act = act;
   if (split > 1) return launch_gemm_split<false, false, kGatedBwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceDGlu);
   const int raster_n_fast = T > ffn ? 1 : 0;
-  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, ffn);
+  const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, ffn, h);
 #define GB_DGLU(PAIR_, WIDE_)                                                                                         \
   launch_gemm_t<false, false, PAIR_, false, WIDE_, kGatedBwd>(st, mA, mB, mC, mOut, mIn, T, ffn, h, e, raster_n_fast, 0, \
                                                               0, stream, kTraceDGlu, 1, 1, kCausalNone, false, false)

@@ -120,11 +120,11 @@ __device__ __forceinline__ void gs_glu(const EpiParams& ep, int64_t row, int col
 }
 
 // Operand layouts and GATED as for k_gemm_bf16_tc.  Grid tiles * 2 * split, clusters of
-// 2 * split CTAs; tile t is row block t % num_m, column block t / num_m.
+// 2 * split CTAs; late_wait as there; tile t is row block t % num_m, column block t / num_m.
 template <bool A_MN, bool B_MN, int GATED>
 __global__ void __launch_bounds__(kGsThreads, 1)
     k_gemm_split(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, int M, int N, int K,
-                 EpiParams ep, int split, int num_m, int* status) {
+                 EpiParams ep, int split, int num_m, int late_wait, int* status) {
   constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kGsThreads, 1)
   cluster_sync();  // every barrier of the cluster is initialised
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  grid_dependency_wait();
+  if (!late_wait) grid_dependency_wait();
   grid_launch_dependents();
 
   if (warp == 0) {
@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kGsThreads, 1)
     tc_fence_after();
     tmem_dealloc<true>(tmem, kBN);
   }
+  if (late_wait) grid_dependency_wait();
 }
 
 }  // namespace gbmlp
