@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "block_math.cuh"
 #include "gemm_tc.cuh"
 #include "ptx.cuh"
 
@@ -55,15 +56,6 @@ constexpr size_t kFaSmemBytes = (size_t)kFaTileBytes * (1 + kFaStages) + 2 * kFa
                                 256 /*barriers*/ + 2 * 2 * 128 * 2 * sizeof(float);
 static_assert(kFaSmemBytes <= 232448, "smem budget");
 static_assert(2 * kFaOStageBytes <= 32 * 128, "O staging fits in a warp's rows of a P buffer");
-constexpr float kLog2e = 1.4426950408889634f;      // log2(e): exp(x) = 2^(x log2 e)
-
-// 2^x with the hardware approximation (ex2.approx, flush-to-zero); 2^-inf = 0.
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 struct FaParams {
   int L;          // sequence length (keys and queries per sequence)
   int nh;         // heads

@@ -50,38 +50,47 @@ __device__ __forceinline__ float gelu_prime_f(float x) {
   return fmaf(2.0f * x * ds, (e * r) * r, r);
 }
 
-// ---- gates of the gated feed-forward block: act(x) and its derivative, a NaN staying a NaN
+// ---- gates of the gated feed-forward block: act(x) and its derivative
+//
+// act(x) = x r, r = 1 / (1 + exp(-z)), with z = x (SiLU) or z = 2 sqrt(2/pi) (x + 0.044715 x^3)
+// (GeLU's tanh form: 0.5 (1 + tanh(z / 2)) = r); derivative r (1 + x z'(x) (1 - r)).
+// No clamp is needed: exp(-z) runs to infinity or 0, r to 0 or 1, and x r to 0 or x; a NaN
+// stays one.  Only x z'(x) of GeLU would overflow where 1 - r is 0, so it is formed from x
+// held within +-30 (1 - r or r is 0 beyond).  The epilogues are bound by instructions:
+// these are 5 to 10 an element, two of them in the special-function unit.
 enum GluAct : int { kActSilu = 0, kActGelu = 1 };
 
-// x * sig(x), sig(x) = r = 1 / (1 + e), e = exp(-x): below x = -80 the value is under
-// 2e-33 in magnitude, and e is held at exp(80) there so that it stays finite.
-// derivative: r + x r (1 - r), with 1 - r = e r.
+constexpr float kLog2e = 1.4426950408889634f;      // log2(e): exp(x) = 2^(x log2 e)
+
+// 2^x with the hardware approximation (ex2.approx, flush-to-zero); 2^-inf = 0.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// r of SiLU
+__device__ __forceinline__ float silu_sig(float x) { return rcp_approx(1.0f + ex2_approx(-kLog2e * x)); }
+// r of GeLU; x2 = x^2
+__device__ __forceinline__ float gelu_sig(float x, float x2) {
+  constexpr float c0 = -2.0f * kLog2e * kSqrt2OverPi, c1 = c0 * kGeluCubic;
+  return rcp_approx(1.0f + ex2_approx(x * fmaf(c1, x2, c0)));
+}
+
+__device__ __forceinline__ float silu_f(float x) { return x * silu_sig(x); }
+__device__ __forceinline__ float gelu_gate_f(float x) { return x * gelu_sig(x, x * x); }
+
 __device__ __forceinline__ void silu_both_f(float x, float& v, float& dv) {
-  const float e = __expf(fminf(-x, 80.0f));
-  const float r = rcp_approx(1.0f + e);
-  const float xr = fmaxf(x, -80.0f) * r;
-  v = x == x ? xr : x;
-  dv = x == x ? fmaf(e * r, fminf(xr, 80.0f), r) : x;
+  const float r = silu_sig(x);
+  v = x * r;
+  dv = r * fmaf(x, 1.0f - r, 1.0f);
 }
-__device__ __forceinline__ float silu_f(float x) {
-  const float v = fmaxf(x, -80.0f) * rcp_approx(1.0f + __expf(fminf(-x, 80.0f)));
-  return x == x ? v : x;
-}
-__device__ __forceinline__ float gelu_gate_f(float x) {
-  const float v = gelu_f(x);
-  return x == x ? v : x;
-}
-// gelu_f and gelu_prime_f sharing their exponential.
 __device__ __forceinline__ void gelu_both_f(float x, float& v, float& dv) {
-  const float xn = fmaxf(x, -30.0f);
-  const float xc = fminf(xn, 30.0f);
-  const float x2 = xc * xc;
-  const float s = kSqrt2OverPi * fmaf(kGeluCubic * xc, x2, xc);
-  const float ds = kSqrt2OverPi * fmaf(3.0f * kGeluCubic, x2, 1.0f);
-  const float e = __expf(fminf(-2.0f * s, 80.0f));
-  const float r = rcp_approx(1.0f + e);
-  v = x == x ? xn * r : x;
-  dv = x == x ? fmaf(2.0f * xc * ds, (e * r) * r, r) : x;
+  const float r = gelu_sig(x, x * x);
+  const float xc = fminf(fmaxf(x, -30.0f), 30.0f);
+  const float z1 = xc * fmaf(6.0f * kSqrt2OverPi * kGeluCubic, xc * xc, 2.0f * kSqrt2OverPi);
+  v = x * r;
+  dv = r * fmaf(z1, 1.0f - r, 1.0f);
 }
 
 __device__ __forceinline__ uint64_t splitmix64_at(uint64_t seed, uint64_t e) {

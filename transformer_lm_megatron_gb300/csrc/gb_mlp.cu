@@ -119,7 +119,7 @@ struct DeviceState {
   bool gemm_attr[96] = {};  // per GEMM instantiation: dynamic smem attribute set
   bool fa_attr = false;     // fused attention core: dynamic smem attribute set
   bool fb_attr = false;     // fused attention backward core: dynamic smem attribute set
-  int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 1) CTAs; [0]: set up
+  int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 2) CTAs; last: set up
   bool few_attr[4] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two

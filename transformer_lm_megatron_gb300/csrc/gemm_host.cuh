@@ -290,15 +290,17 @@ bool few_waves(const DeviceState* st, int M, int64_t cols, int K) {
   return (K + kBK - 1) / kBK < 64 && (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
 }
 
-// The pairs to share one tile's reduction among (k_gemm_split), or 1 where the tiles fill
-// the SMs by themselves.  Each pair has 6 k-blocks or more, as many as its ring holds.
+// The pairs to share one tile's reduction among (k_gemm_split), or 0 where the tiles fill
+// the SMs by themselves.  Each pair has 6 k-blocks or more, as many as its ring holds.  (One
+// pair to a tile there is no faster than the persistent kernel: 42 and 40 us for the input
+// gradient at 1024 tokens, h 1024, ffn 4096.)
 template <bool AM, bool BM, int GATED>
 int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
-  *split = 1;
+  *split = 0;
   if (g_pair_mode.load(std::memory_order_relaxed) == 0) return MLP_OK;
   auto kern = k_gemm_split<AM, BM, GATED>;
   int* clusters = st->split_clusters[(AM ? 2 : 0) + (BM ? 1 : 0) + 4 * GATED];
-  if (clusters[0] == 0) {
+  if (clusters[kGsMaxSplit - 1] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGsSmemBytes);
     if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (split GEMM): %s", cudaGetErrorString(e));
     for (int s = 2; s <= kGsMaxSplit; ++s) {
@@ -317,14 +319,14 @@ int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
         cudaGetLastError();
         n = 0;
       }
-      clusters[s - 1] = n;
+      clusters[s - 2] = n;
     }
-    clusters[0] = 1;
+    clusters[kGsMaxSplit - 1] = 1;  // set up
   }
   const int64_t tiles = (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN);
   const int num_kb = (K + kBK - 1) / kBK;
   for (int s = kGsMaxSplit; s >= 2; --s)
-    if (tiles <= clusters[s - 1] && num_kb >= kGsStages * s) {
+    if (tiles <= clusters[s - 2] && num_kb >= kGsStages * s) {
       *split = s;
       break;
     }
@@ -349,10 +351,10 @@ int launch_gemm_split(DeviceState* st, const CUtensorMap& mA, const CUtensorMap&
 template <bool AM, bool BM>
 int gemm_block(DeviceState* st, const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int M, int N, int K,
                const EpiParams& ep, cudaStream_t stream, int trace_kind, bool late_wait = false) {
-  int split = 1;
+  int split = 0;
   int rc = split_pairs<AM, BM, kGatedNone>(st, M, N, K, &split);
   if (rc) return rc;
-  if (split == 1)  // ((MN, K) is not instantiated with 8 epilogue warps)
+  if (split == 0)  // ((MN, K) is not instantiated with 8 epilogue warps)
     return gemm(st, a, AM, lda, b, BM, ldb, M, N, K, ep, stream, trace_kind, late_wait, false,
                 few_waves(st, M, N, K) && (!AM || BM));
   CUtensorMap mA, mB;
@@ -384,10 +386,10 @@ int gemm_glu(DeviceState* st, const uint16_t* X, const uint16_t* A, const uint16
   e.out1 = Y;
   e.bias = a;
   e.act = act;
-  int split = 1;
+  int split = 0;
   rc = split_pairs<false, true, kGatedFwd>(st, T, 2 * (int64_t)ffn, h, &split);
   if (rc) return rc;
-  if (split > 1) return launch_gemm_split<false, true, kGatedFwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceGlu);
+  if (split > 0) return launch_gemm_split<false, true, kGatedFwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceGlu);
   const int raster_n_fast = T > 2 * (int64_t)ffn ? 1 : 0;
   const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, 2 * (int64_t)ffn, h);
 #define GB_GLU(PAIR_, WIDE_)                                                                                          \
@@ -402,7 +404,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
               int h, int act, cudaStream_t stream) {
   const int mode = g_pair_mode.load(std::memory_order_relaxed);
   const bool pair = mode == 1 || (mode < 0 && T > kBM);
-  int split = 1;
+  int split = 0;
   int rc = split_pairs<false, false, kGatedBwd>(st, T, ffn, h, &split);
   if (rc) return rc;
   CUtensorMap mA, mB, mC, mOut, mIn;
@@ -411,7 +413,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
   // (a CTA of a pair loads half of a tile's columns, whichever kernel it runs)
   if (!rc)
     rc = operand_map(&mB, B, false, ffn, h, h,
-                     pair || split > 1 ? GemmCfg<true>::kBLoadN : GemmCfg<false>::kBLoadN);
+                     pair || split > 0 ? GemmCfg<true>::kBLoadN : GemmCfg<false>::kBLoadN);
   if (!rc)
     rc = make_half_map(&mOut, dGU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
   if (!rc) rc = make_half_map(&mIn, GU, ffn, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
@@ -421,7 +423,7 @@ int gemm_dglu(DeviceState* st, const uint16_t* dZ, const uint16_t* B, const uint
   e.out0 = dGU;
   e.in0 = GU;
   e.act = act;
-  if (split > 1) return launch_gemm_split<false, false, kGatedBwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceDGlu);
+  if (split > 0) return launch_gemm_split<false, false, kGatedBwd>(st, mA, mB, T, ffn, h, e, split, stream, kTraceDGlu);
   const int raster_n_fast = T > ffn ? 1 : 0;
   const bool wide = (h + kBK - 1) / kBK < 16 || few_waves(st, T, ffn, h);
 #define GB_DGLU(PAIR_, WIDE_)                                                                                         \

@@ -25,6 +25,7 @@ constexpr int kGsStages = 6;
 constexpr int kGsPitch = kBN + 4;  // floats: rows 16 bytes off each other's banks
 constexpr uint32_t kGsStageBytes = kABytes + (kBN / 2) * kBK * 2;
 constexpr int kGsMaxSplit = 4;
+constexpr int kGsBatch = 4;        // items of a thread whose inputs are fetched together
 constexpr size_t kGsSmemBytes = (size_t)kGsStages * kGsStageBytes + 1024;
 static_assert(kBM * kGsPitch * 4 <= kGsStages * kGsStageBytes, "the partial fits the ring");
 
@@ -42,24 +43,42 @@ __device__ __forceinline__ void gs_sum8(uint32_t at, int split, uint32_t half, f
   }
 }
 
-// One item of the epilogue: 8 columns of one row, v = their sums.
-__device__ __forceinline__ void gs_epilogue(const EpiParams& ep, int64_t row, int col, int N, float (&v)[8]) {
+__device__ __forceinline__ void unpack_bf16x8(const uint4& q, float (&v)[8]) {
+  v[0] = bf16lo(q.x), v[1] = bf16hi(q.x), v[2] = bf16lo(q.y), v[3] = bf16hi(q.y);
+  v[4] = bf16lo(q.z), v[5] = bf16hi(q.z), v[6] = bf16lo(q.w), v[7] = bf16hi(q.w);
+}
+
+// One item of the epilogue is 8 columns of one row.  What it reads from global memory is
+// fetched for several items before the first is worked on: a = the residual, or G, and b = U.
+__device__ __forceinline__ void gs_fetch(const EpiParams& ep, int64_t row, int col, int N, uint4& a, uint4& b) {
+  if (ep.kind == kEpiDGlu) {
+    const uint16_t* p = ep.in0 + row * 2 * N + col;
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *reinterpret_cast<const uint4*>(p + N);
+  } else if (ep.kind == kEpiDropRes || (ep.kind == kEpiResAdd && ep.in0 != nullptr)) {
+    a = *reinterpret_cast<const uint4*>(ep.in0 + row * ep.ld + col);
+  }
+}
+
+// v = the item's sums.
+__device__ __forceinline__ void gs_epilogue(const EpiParams& ep, int64_t row, int col, int N, const uint4& a,
+                                            const uint4& b, float (&v)[8]) {
   const int64_t off = row * ep.ld + col;
   float x[8];
   switch (ep.kind) {
     case kEpiDropRes: {
-      float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (ep.bias != nullptr) ld_bf16x8(ep.bias + col, b);
-      ld_bf16x8(ep.in0 + off, x);
+      float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (ep.bias != nullptr) ld_bf16x8(ep.bias + col, bias);
+      unpack_bf16x8(a, x);
       const uint32_t keep = ep.drop.thr == 0 ? 0xffu : dropout_keep8(ep.drop, row, col);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = x[j] + (((keep >> j) & 1u) ? (v[j] + b[j]) * ep.drop.scale : 0.0f);
+      for (int j = 0; j < 8; ++j) v[j] = x[j] + (((keep >> j) & 1u) ? (v[j] + bias[j]) * ep.drop.scale : 0.0f);
       st_bf16x8(ep.out0 + off, v);
       break;
     }
     case kEpiResAdd:
       if (ep.in0 != nullptr) {
-        ld_bf16x8(ep.in0 + off, x);
+        unpack_bf16x8(a, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += x[j];
       }
@@ -68,8 +87,8 @@ __device__ __forceinline__ void gs_epilogue(const EpiParams& ep, int64_t row, in
     case kEpiDGlu: {
       float g[8], u[8], dg[8], du[8];
       const int64_t at = row * 2 * N + col;
-      ld_bf16x8(ep.in0 + at, g);
-      ld_bf16x8(ep.in0 + at + N, u);
+      unpack_bf16x8(a, g);
+      unpack_bf16x8(b, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float value, slope;
@@ -86,14 +105,14 @@ __device__ __forceinline__ void gs_epilogue(const EpiParams& ep, int64_t row, in
     }
     default: {  // kEpiF32Store, kEpiF32Add
       float4* p = reinterpret_cast<float4*>(ep.g_out + off);
-      float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
+      float4 s = make_float4(v[0], v[1], v[2], v[3]), t = make_float4(v[4], v[5], v[6], v[7]);
       if (ep.kind == kEpiF32Add) {
         const float4 c = p[0], d = p[1];
-        a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-        b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+        s.x += c.x, s.y += c.y, s.z += c.z, s.w += c.w;
+        t.x += d.x, t.y += d.y, t.z += d.z, t.w += d.w;
       }
-      p[0] = a;
-      p[1] = b;
+      p[0] = s;
+      p[1] = t;
     }
   }
 }
@@ -275,22 +294,34 @@ __global__ void __launch_bounds__(kGsThreads, 1)
   }
   __syncthreads();
   cluster_sync();
-  // This CTA's share of the rows, 8 columns an item.
+  // This CTA's share of the rows, 8 columns an item, kGsBatch items of a thread at a time.
   const int r_begin = kBM * q / split, r_end = min(kBM * (q + 1) / split, M - m0);
   constexpr int kItems = kTileN / 8;
+  const int items = max(r_end - r_begin, 0) * kItems;
   const uint32_t base = smem_u32(partial);
-  for (int i = threadIdx.x; i < (r_end - r_begin) * kItems; i += kGsThreads) {
-    const int r = r_begin + i / kItems, c = (i % kItems) * 8, col = n0 + c;
-    if (col >= N) continue;
-    const uint32_t at = base + (uint32_t)(r * kGsPitch + c) * 4;
-    float v[8];
-    gs_sum8(at, split, half, v);
-    if constexpr (GATED == kGatedFwd) {
-      float u[8];
-      gs_sum8(at + kTileN * 4, split, half, u);
-      gs_glu(ep, (int64_t)m0 + r, col, N, v, u);
-    } else {
-      gs_epilogue(ep, (int64_t)m0 + r, col, N, v);
+  for (int i0 = threadIdx.x; i0 < items; i0 += kGsBatch * kGsThreads) {
+    uint4 a[kGsBatch], b[kGsBatch];
+    if constexpr (GATED != kGatedFwd) {
+#pragma unroll
+      for (int k = 0; k < kGsBatch; ++k) {
+        const int i = i0 + k * kGsThreads, col = n0 + (i % kItems) * 8;
+        if (i < items && col < N) gs_fetch(ep, (int64_t)m0 + r_begin + i / kItems, col, N, a[k], b[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kGsBatch; ++k) {
+      const int i = i0 + k * kGsThreads, r = r_begin + i / kItems, c = (i % kItems) * 8, col = n0 + c;
+      if (i >= items || col >= N) continue;
+      const uint32_t at = base + (uint32_t)(r * kGsPitch + c) * 4;
+      float v[8];
+      gs_sum8(at, split, half, v);
+      if constexpr (GATED == kGatedFwd) {
+        float u[8];
+        gs_sum8(at + kTileN * 4, split, half, u);
+        gs_glu(ep, (int64_t)m0 + r, col, N, v, u);
+      } else {
+        gs_epilogue(ep, (int64_t)m0 + r, col, N, a[k], b[k], v);
+      }
     }
   }
   cluster_sync();  // the peers have read this CTA's partial, and the pair's MMAs its shared memory

@@ -279,21 +279,21 @@ __device__ __forceinline__ void epilogue_values(const EpiParams& ep, int64_t row
   }
 }
 
-// Gated forward epilogue of one row, 32 columns [col0, col0 + 32): adds the biases to
-// G and U in place and packs Y = act(G) * U, formed from the fp32 values.
-__device__ __forceinline__ void glu_epilogue(const EpiParams& ep, int col0, int N, uint32_t (&g)[32], uint32_t (&u)[32],
-                                             uint32_t (&y)[16]) {
+// Gated forward epilogue of one row, 32 columns: adds the biases (32 packed bf16 each, or
+// null) to G and U in place and packs Y = act(G) * U, formed from the fp32 values.
+__device__ __forceinline__ void glu_epilogue(const EpiParams& ep, const uint4 (&bg)[4], const uint4 (&bu)[4],
+                                             uint32_t (&g)[32], uint32_t (&u)[32], uint32_t (&y)[16]) {
   if (ep.bias != nullptr) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (col0 + 8 * q >= N) continue;
-      float bg[8], bu[8];
-      ld_bf16x8(ep.bias + col0 + 8 * q, bg);
-      ld_bf16x8(ep.bias + N + col0 + 8 * q, bu);
+      const uint32_t wg[4] = {bg[q].x, bg[q].y, bg[q].z, bg[q].w}, wu[4] = {bu[q].x, bu[q].y, bu[q].z, bu[q].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        g[8 * q + j] = __float_as_uint(__uint_as_float(g[8 * q + j]) + bg[j]);
-        u[8 * q + j] = __float_as_uint(__uint_as_float(u[8 * q + j]) + bu[j]);
+      for (int j = 0; j < 4; ++j) {
+        const int e = 8 * q + 2 * j;
+        g[e] = __float_as_uint(__uint_as_float(g[e]) + bf16lo(wg[j]));
+        g[e + 1] = __float_as_uint(__uint_as_float(g[e + 1]) + bf16hi(wg[j]));
+        u[e] = __float_as_uint(__uint_as_float(u[e]) + bf16lo(wu[j]));
+        u[e + 1] = __float_as_uint(__uint_as_float(u[e + 1]) + bf16hi(wu[j]));
       }
     }
   }
@@ -834,12 +834,14 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
       }
       ++n_in;
     };
-    // kGatedBwd: G and U of one column block into the warp's first two boxes
+    // kGatedBwd: G and U of one column block into one of the warp's two pairs of boxes
     auto dglu_request = [&](int x, int y) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(&my_in_full[0], 2 * kOutBoxBf16Bytes);
-        tma_load_3d(my_out, &tmO1, &my_in_full[0], x, 0, y);
-        tma_load_3d(my_out + kOutBoxBf16Bytes, &tmO1, &my_in_full[0], x, 1, y);
+        uint8_t* box = my_out + (n_in & 1) * (2 * kOutBoxBf16Bytes);
+        uint64_t* bar = &my_in_full[n_in & 1];
+        mbar_arrive_expect_tx(bar, 2 * kOutBoxBf16Bytes);
+        tma_load_3d(box, &tmO1, bar, x, 0, y);
+        tma_load_3d(box + kOutBoxBf16Bytes, &tmO1, bar, x, 1, y);
       }
       ++n_in;
     };
@@ -870,9 +872,12 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
       const int n_first = min(n_blocks, kInDepth);
       for (int q = 0; q < n_first; ++q) request_in(n0 + col_begin + 32 * q, m0 + quarter * 32, hb, sb);
       if constexpr (GATED == kGatedBwd) {
-        // the first block's G and U; a split tail's half that turns out not to write
-        // its output (below) waits for them all the same
-        if (rows_in && n0 + col_begin < N) dglu_request(n0 + col_begin, m0 + quarter * 32);
+        // G and U of the first two blocks, ahead of the accumulator
+        if (rows_in && n0 + col_begin < N) {
+          if (lane == 0) bulk_wait_read<0>();  // the last tile's outputs have left the boxes
+          dglu_request(n0 + col_begin, m0 + quarter * 32);
+          if (col_begin + 32 < col_end && n0 + col_begin + 32 < N) dglu_request(n0 + col_begin + 32, m0 + quarter * 32);
+        }
       }
       if (!(PAIR ? mbar_wait_cluster(&acc_full[acc], acc_phase) : mbar_wait(&acc_full[acc], acc_phase))) {
         record_status(status, kStatusTimeout, 6);
@@ -912,10 +917,6 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
         } else {
           // no output from this half: retire the input boxes requested for it
           for (int q = 0; q < n_first; ++q) wait_in(n_in_used++);
-          if constexpr (GATED == kGatedBwd) {
-            if (rows_in && n0 + col_begin < N && !mbar_wait(&my_in_full[0], (n_in - 1) & 1))
-              record_status(status, kStatusTimeout, 7);
-          }
         }
       }
       // One column block (32 columns) of this warp's rows: r holds its accumulator.
@@ -936,18 +937,6 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
           __syncwarp();
         }
       };
-      // the other half's partial sums of the accumulator columns [c, c + 32) (split tail)
-      auto add_other = [&](int c, uint32_t (&r)[32]) {
-        if (other == nullptr) return;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(other + c + 4 * j));
-          r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + o.x);
-          r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + o.y);
-          r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + o.z);
-          r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + o.w);
-        }
-      };
       // 32 packed bf16 of this lane's row into a 32 x 32 box with the 64-byte swizzle
       auto fill_box = [&](uint8_t* box, const uint32_t (&o)[16]) {
 #pragma unroll
@@ -955,81 +944,93 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
           *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       };
-      // kGatedFwd: G, U (if wanted) and Y of 32 rows x 32 columns.  Each output box
-      // leaves as a bulk group of its own through a ring of the warp's four boxes.
+      // kGatedFwd: G, U (if wanted) and Y of 32 rows x 32 columns, in three of the warp's
+      // four boxes.
       auto glu_block = [&](int c0) {
         if (n0 + c0 >= N || m0 + quarter * 32 >= M) return;
+        uint4 bg[4], bu[4];  // asked for ahead of the accumulator
+        if (ep.bias != nullptr) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = min(n0 + c0 + 8 * q, N - 8);  // (columns past N are clipped)
+            bg[q] = *reinterpret_cast<const uint4*>(ep.bias + col);
+            bu[q] = *reinterpret_cast<const uint4*>(ep.bias + N + col);
+          }
+        }
         uint32_t g[32], u[32], y[16];
         tmem_ld_32x32b_x32(t_row + c0, g);
         tmem_ld_32x32b_x32(t_row + kTileN + c0, u);
         tmem_ld_wait();
-        add_other(c0, g);
-        add_other(kTileN + c0, u);
-        glu_epilogue(ep, n0 + c0, N, g, u, y);
-        auto put = [&](const CUtensorMap* map, int half, const uint32_t (&o)[16]) {
-          uint8_t* box = my_out + (n_out & 3) * kOutBoxBf16Bytes;
-          if (lane == 0) bulk_wait_read<3>();
-          __syncwarp();
-          fill_box(box, o);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (half < 0)
-              tma_store_2d(map, box, n0 + c0, m0 + quarter * 32, 0, false);
-            else
-              tma_store_3d(map, box, n0 + c0, half, m0 + quarter * 32);
-            bulk_commit();
-          }
-          ++n_out;
-        };
+        glu_epilogue(ep, bg, bu, g, u, y);
+        if (lane == 0) bulk_wait_read<0>();  // the block before has left the boxes
+        __syncwarp();
         if (ep.out0 != nullptr) {
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-          put(&tmO0, 0, o);
+          fill_box(my_out, o);
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-          put(&tmO0, 1, o);
+          fill_box(my_out + kOutBoxBf16Bytes, o);
         }
-        put(&tmO1, -1, y);
+        fill_box(my_out + 2 * kOutBoxBf16Bytes, y);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (ep.out0 != nullptr) {
+            tma_store_3d(&tmO0, my_out, n0 + c0, 0, m0 + quarter * 32);
+            tma_store_3d(&tmO0, my_out + kOutBoxBf16Bytes, n0 + c0, 1, m0 + quarter * 32);
+          }
+          tma_store_2d(&tmO1, my_out + 2 * kOutBoxBf16Bytes, n0 + c0, m0 + quarter * 32, 0, false);
+          bulk_commit();
+        }
       };
-      // kGatedBwd: dG and dU of 32 rows x 32 columns.  The warp's first two boxes
-      // receive the block's G and U, the other two its outputs.
+      // kGatedBwd: dG and dU of 32 rows x 32 columns, written over the G and U they come
+      // from: a lane reads and writes its own row of the two boxes.
       auto dglu_block = [&](int c0) {
         if (n0 + c0 >= N || m0 + quarter * 32 >= M) return;
         uint32_t r[32], gp[16], up[16];
         tmem_ld_32x32b_x32(t_row + c0, r);
         tmem_ld_wait();
-        add_other(c0, r);
-        if (!mbar_wait(&my_in_full[0], (n_in - 1) & 1)) record_status(status, kStatusTimeout, 7);
+        uint8_t* box = my_out + (n_out & 1) * (2 * kOutBoxBf16Bytes);
+        if (!mbar_wait(&my_in_full[n_out & 1], (n_out >> 1) & 1)) record_status(status, kStatusTimeout, 7);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t off = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
-          const uint4 a = *reinterpret_cast<const uint4*>(my_out + off);
-          const uint4 b = *reinterpret_cast<const uint4*>(my_out + kOutBoxBf16Bytes + off);
+          const uint4 a = *reinterpret_cast<const uint4*>(box + off);
+          const uint4 b = *reinterpret_cast<const uint4*>(box + kOutBoxBf16Bytes + off);
           gp[4 * j] = a.x, gp[4 * j + 1] = a.y, gp[4 * j + 2] = a.z, gp[4 * j + 3] = a.w;
           up[4 * j] = b.x, up[4 * j + 1] = b.y, up[4 * j + 2] = b.z, up[4 * j + 3] = b.w;
         }
-        if (c0 + 32 < col_end && n0 + c0 + 32 < N) {
-          fence_proxy_async_smem();  // every lane has read the boxes before they are refilled
-          __syncwarp();
+        // The other pair of boxes, whose stores are the last group, takes the next block but
+        // the first two's.
+        if (c0 > col_begin && c0 + 32 < col_end && n0 + c0 + 32 < N) {
+          if (lane == 0) bulk_wait_read<0>();
           dglu_request(n0 + c0 + 32, m0 + quarter * 32);
         }
         dglu_epilogue(ep, r, gp, up);  // gp, up become dG, dU
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        fill_box(my_out + 2 * kOutBoxBf16Bytes, gp);
-        fill_box(my_out + 3 * kOutBoxBf16Bytes, up);
+        fill_box(box, gp);
+        fill_box(box + kOutBoxBf16Bytes, up);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&tmO0, my_out + 2 * kOutBoxBf16Bytes, n0 + c0, 0, m0 + quarter * 32);
-          tma_store_3d(&tmO0, my_out + 3 * kOutBoxBf16Bytes, n0 + c0, 1, m0 + quarter * 32);
+          tma_store_3d(&tmO0, box, n0 + c0, 0, m0 + quarter * 32);
+          tma_store_3d(&tmO0, box + kOutBoxBf16Bytes, n0 + c0, 1, m0 + quarter * 32);
           bulk_commit();
         }
+        ++n_out;
       };
       auto out_block = [&](int c0, uint32_t (&r)[32]) {
-        add_other(c0, r);
+        if (other != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(other + c0 + 4 * j));
+            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + o.x);
+            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + o.y);
+            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + o.z);
+            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + o.w);
+          }
+        }
         if (tma_out) {
           // Warp-uniform: this warp's 32 rows x 32 columns go out as one TMA box;
           // rows >= M and columns >= N are clipped by the tensor map.

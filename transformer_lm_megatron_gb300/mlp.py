@@ -174,7 +174,7 @@ def attn_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, residual_grad, ac
 # ---------------------------------------------------------------------------
 GLU_SILU, GLU_GELU = 0, 1
 _bf16, _float, _int = torch.bfloat16, torch.float32, torch.int32
-_device = torch.cuda.current_device
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -214,7 +214,7 @@ def _rows(name, t, shape, dev):
         _refuse(name, t, _bf16, shape, dev)
     row, head, one = t.stride()
     tokens, heads, d = shape
-    if one != 1 and d > 1 or head != d and heads > 1:
+    if (one != 1 and d > 1) or (head != d and heads > 1):
         _refuse(name, t, _bf16, shape, dev)
     return t.data_ptr(), row if tokens > 1 else heads * d
 
@@ -285,10 +285,17 @@ def qk_norm_rope_fwd(Q, K, Qo, Ko, pos, inv_freq, wq=None, wk=None, eps=1e-6, ro
     Qo and Ko.  pos [axes, tokens] int32, inv_freq [rot / 2] fp32, sections: the pairs of each axis."""
     dev = _device()
     T, nq, d = qs = Q.shape
-    ks = (T, K.shape[1], d)
-    _check(load().qk_norm_rope_fwd(T, nq, ks[1], d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev),
-                                   *_rows("Q", Q, qs, dev), *_rows("K", K, ks, dev), *_rows("Qo", Qo, qs, dev),
-                                   *_rows("Ko", Ko, ks, dev), _here(dev, stream)))
+    nk = K.shape[1]
+    ks = (T, nk, d)
+    q, ldq = _rows("Q", Q, qs, dev)
+    k, ldk = _rows("K", K, ks, dev)
+    qo, ldqo = _rows("Qo", Qo, qs, dev)
+    ko, ldko = _rows("Ko", Ko, ks, dev)
+    rc = (_lib or load()).qk_norm_rope_fwd(
+        T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev), q, ldq, k, ldk, qo, ldqo,
+        ko, ldko, _here(dev, stream))
+    if rc:
+        _check(rc)
 
 
 def qk_norm_rope_bwd(Q, K, dQo, dKo, dQ, dK, pos, inv_freq, wq=None, wk=None, dwq=None, dwk=None, ws=None, eps=1e-6,
@@ -297,13 +304,19 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, dQ, dK, pos, inv_freq, wq=None, wk=None, dw
     qk_norm_rope_workspace(d) floats).  Without the norm Q and K may be None."""
     dev = _device()
     T, nq, d = qs = dQo.shape
-    ks = (T, dKo.shape[1], d)
-    norm = wq is not None
-    _check(load().qk_norm_rope_bwd(T, nq, ks[1], d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev),
-                                   int(accumulate), *(_rows("Q", Q, qs, dev) if norm else (None, 0)),
-                                   *(_rows("K", K, ks, dev) if norm else (None, 0)), *_rows("dQo", dQo, qs, dev),
-                                   *_rows("dKo", dKo, ks, dev), *_rows("dQ", dQ, qs, dev), *_rows("dK", dK, ks, dev),
-                                   *_dw_args(d, wq, dwq, dwk, ws, dev), _here(dev, stream)))
+    nk = dKo.shape[1]
+    ks = (T, nk, d)
+    q, ldq = (None, 0) if wq is None else _rows("Q", Q, qs, dev)
+    k, ldk = (None, 0) if wq is None else _rows("K", K, ks, dev)
+    gq, ldgq = _rows("dQo", dQo, qs, dev)
+    gk, ldgk = _rows("dKo", dKo, ks, dev)
+    oq, ldoq = _rows("dQ", dQ, qs, dev)
+    ok, ldok = _rows("dK", dK, ks, dev)
+    rc = (_lib or load()).qk_norm_rope_bwd(
+        T, nq, nk, d, *_rope_args(T, d, pos, inv_freq, wq, wk, rot, sections, interleaved, eps, dev), 1 if accumulate else 0,
+        q, ldq, k, ldk, gq, ldgq, gk, ldgk, oq, ldoq, ok, ldok, *_dw_args(d, wq, dwq, dwk, ws, dev), _here(dev, stream))
+    if rc:
+        _check(rc)
 
 
 class Rope:
