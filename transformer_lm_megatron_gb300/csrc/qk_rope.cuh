@@ -18,8 +18,8 @@
 // pairs, so a lane needs no other lane's elements to turn its own, and a warp holds
 // several heads at once (d = 128: 4 heads of 8 lanes): a step.  The steps of all tokens in
 // a row are shared out over the warps evenly (whole tokens to a warp left a third of the
-// SMs idle at 2048 tokens); a warp forms the sines and cosines of its lanes' pairs once
-// for each token that it comes to.  The heads
+// SMs idle at 2048 tokens); a warp forms the sines and cosines of a token's pairs once,
+// its lanes a share each, for each token that it comes to.  The heads
 // come through a ring in shared memory, several steps ahead and across tokens; a lane
 // reads back only what it copied itself, so the ring needs no barrier.  Arithmetic is
 // fp32, two values an instruction; outputs are rounded once.
@@ -231,26 +231,23 @@ struct QkPos {
   }
 };
 
-// What a warp keeps in shared memory besides its ring, one value per lane.
-template <int VEC>
-struct QkWarpSmem {
-  float cs[VEC][32], sn[VEC][32];  // of the lane's pairs at the current token
+constexpr int kQkPairs = kQkMaxHead / 2;  // most pairs of a head
+
+// The cosines and sines of a token's pairs, in a warp's shared memory.
+struct QkAngles {
+  float cs[kQkPairs], sn[kQkPairs];
 };
 
-// Sines and cosines of a lane's VEC pairs at position x; `turn`: the CTA's frequencies.
-template <int VEC>
-__device__ __forceinline__ void qk_angles(const QkPos& x, const uint64_t (*turn)[32], uint32_t axes, bool turns,
-                                          QkWarpSmem<VEC>& ws) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const uint32_t a = (axes >> (2 * j)) & 3u;
-    const uint64_t phase = (uint64_t)(int64_t)(a == 0 ? x.at[0] : a == 1 ? x.at[1] : x.at[2]) * turn[j][lane];
-    float c, s;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    ws.cs[j][lane] = turns ? c : 1.0f;
-    ws.sn[j][lane] = turns ? s : 0.0f;
+// Fills them for position x: the warp's lanes share out the pairs, whose frequencies are
+// `turn`.
+__device__ __forceinline__ void qk_angles(const QkRopeParams& p, const QkPos& x, const uint64_t* turn, QkAngles& out) {
+  __syncwarp();  // the last token's have been read
+  for (int i = threadIdx.x & 31; i < (p.rot >> 1); i += 32) {
+    const int32_t at = i < p.axis1 ? x.at[0] : i < p.axis2 ? x.at[1] : x.at[2];
+    const uint64_t phase = (uint64_t)(int64_t)at * turn[i];
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &out.sn[i], &out.cs[i]);
   }
+  __syncwarp();
 }
 
 // The turn of a lane's two vectors x as out[v] = own P[v] + partner Q[v], two elements a
@@ -258,21 +255,27 @@ __device__ __forceinline__ void qk_angles(const QkPos& x, const uint64_t (*turn)
 // (interleaved) its neighbour.  sign 1 turns forwards; w[v]: the elements' weights
 // (NORM), multiplied in.
 template <int VEC, bool INTER, bool WEIGHTS>
-__device__ __forceinline__ void qk_turn_terms(const QkWarpSmem<VEC>& ws, float sign, const QkVec<VEC> (&w)[2],
-                                              uint64_t (&P)[2][VEC / 2], uint64_t (&Q)[2][VEC / 2]) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void qk_turn_terms(const QkAngles& angles, const QkLane<VEC, INTER>& L, float sign,
+                                              const QkVec<VEC> (&w)[2], uint64_t (&P)[2][VEC / 2],
+                                              uint64_t (&Q)[2][VEC / 2]) {
+  float cs[VEC], sn[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    cs[j] = L.turns ? angles.cs[VEC * L.li + j] : 1.0f;
+    sn[j] = L.turns ? angles.sn[VEC * L.li + j] : 0.0f;
+  }
 #pragma unroll
   for (int v = 0; v < 2; ++v)
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
       const float w0 = WEIGHTS ? w[v].at(2 * j) : 1.0f, w1 = WEIGHTS ? w[v].at(2 * j + 1) : 1.0f;
       if constexpr (INTER) {
-        const float c = ws.cs[v * VEC / 2 + j][lane], s = sign * ws.sn[v * VEC / 2 + j][lane];
+        const float c = cs[v * VEC / 2 + j], s = sign * sn[v * VEC / 2 + j];
         P[v][j] = f2(w0 * c, w1 * c);
         Q[v][j] = f2(-w1 * s, w0 * s);
       } else {
-        const float c0 = ws.cs[2 * j][lane], c1 = ws.cs[2 * j + 1][lane];
-        const float s0 = (v ? sign : -sign) * ws.sn[2 * j][lane], s1 = (v ? sign : -sign) * ws.sn[2 * j + 1][lane];
+        const float c0 = cs[2 * j], c1 = cs[2 * j + 1];
+        const float s0 = (v ? sign : -sign) * sn[2 * j], s1 = (v ? sign : -sign) * sn[2 * j + 1];
         const float u0 = WEIGHTS ? w[v ^ 1].at(2 * j) : 1.0f, u1 = WEIGHTS ? w[v ^ 1].at(2 * j + 1) : 1.0f;
         P[v][j] = f2(w0 * c0, w1 * c1);
         Q[v][j] = f2(u0 * s0, u1 * s1);
@@ -312,10 +315,11 @@ __device__ __forceinline__ void qk_pack_store(uint16_t* dst, const uint64_t (&f)
 
 // Steps in a warp's ring: the one at work and those on their way.  2048 x 256 heads of 160
 // forward (336 MB: 49 us at the copy rate): 123 us with the loads of one step straight into
-// registers, 75 us with four steps in registers; with the ring 57 us at 4 steps, 63 at 5
-// and 8, 57 at 12.  8209 x 40 heads of 128 backward (252 MB: 37 us): 48 us at 3 steps, 57 at 2.
+// registers, 75 us with four steps in registers; with the ring 57 us at 4 steps, 62 at 6.
+// 8209 x 40 heads of 128 backward (252 MB: 37 us), dw's second launch with it: 47 us at 3
+// or 4 steps, 57 at 2.  What is left is DRAM latency at 16 warps an SM (126 registers; the
+// forward at 24 warps is no faster).
 constexpr int kQkDepth = 4;
-constexpr int kQkDepthBwd = 3;
 
 // Dynamic shared memory of a kernel: the frequencies, every warp's cosines and sines, the
 // sums of dw (backward with the norm), and the rings: per warp DEPTH steps of VECS vectors
@@ -323,11 +327,11 @@ constexpr int kQkDepthBwd = 3;
 template <int VEC, bool BWD, bool NORM>
 struct QkSmem {
   static constexpr int kVecs = BWD && NORM ? 4 : 2;
-  static constexpr int kDepth = BWD ? kQkDepthBwd : kQkDepth;
+  static constexpr int kDepth = kQkDepth;
   static constexpr int kVecBytes = 2 * VEC * 32;  // one vector of every lane
   static constexpr int kTurn = 0;
-  static constexpr int kAngles = kTurn + VEC * 32 * 8;
-  static constexpr int kPart = kAngles + kQkWarps * (int)sizeof(QkWarpSmem<VEC>);
+  static constexpr int kAngles = kTurn + kQkPairs * 8;
+  static constexpr int kPart = kAngles + kQkWarps * (int)sizeof(QkAngles);
   static constexpr int kRing = kPart + (BWD && NORM ? kQkWarps * 2 * 2 * VEC * 32 * 4 : 0);
   static constexpr int kBytes = kRing + kQkWarps * kDepth * kVecs * kVecBytes;
 };
@@ -338,19 +342,13 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
   using Smem = QkSmem<VEC, BWD, NORM>;
   constexpr int D = Smem::kDepth, H = VEC / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint64_t(*turn)[32] = reinterpret_cast<uint64_t(*)[32]>(smem + Smem::kTurn);
+  uint64_t* turn = reinterpret_cast<uint64_t*>(smem + Smem::kTurn);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (uniform to the compiler)
-  QkWarpSmem<VEC>& ws = reinterpret_cast<QkWarpSmem<VEC>*>(smem + Smem::kAngles)[warp];
+  QkAngles& angles = reinterpret_cast<QkAngles*>(smem + Smem::kAngles)[warp];
   // dw of every lane's elements over its warp's tokens: [warp][q | k][element of the lane][lane]
   float* part = reinterpret_cast<float*>(smem + Smem::kPart);
   uint8_t* ring = smem + Smem::kRing + warp * (D * Smem::kVecs * Smem::kVecBytes) + lane * (2 * VEC);
   const QkLane<VEC, INTER> L(p.d, p.rot, lane);
-  uint32_t axes = 0;  // of the lane's pairs, two bits each
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const int i = VEC * L.li + j;
-    if (L.active && L.turns) axes |= (i < p.axis1 ? 0u : i < p.axis2 ? 1u : 2u) << (2 * j);
-  }
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -402,15 +400,14 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
   for (int s = 0; s < D - 1; ++s) fetch();
   QkPos pos;
   if (at.left > 0) pos.load(p, at.token);
-  for (int j = warp; j < VEC; j += kQkWarps)
-    turn[j][lane] = L.active && L.turns ? qk_turns(p.inv_freq[VEC * L.li + j]) : 0;
+  for (int i = threadIdx.x; i < (p.rot >> 1); i += kQkThreads) turn[i] = qk_turns(p.inv_freq[i]);
   float* mine = part + warp * 2 * 2 * VEC * 32 + lane;
   if constexpr (BWD && NORM)
     for (int j = 0; j < 2 * 2 * VEC; ++j) mine[j * 32] = 0.0f;
   __syncthreads();
 
   const float inv_d = 1.0f / (float)p.d;
-  int token = -1;      // whose angles ws holds
+  int token = -1;      // whose angles the warp holds
   int tensor = -1;     // whose terms P and Q hold
   uint32_t slot = 0;
   uint16_t* out = nullptr;
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
     if (at.token != token) {
       token = at.token;
       tensor = -1;
-      qk_angles<VEC>(pos, turn, axes, L.turns, ws);
+      qk_angles(p, pos, turn, angles);
       if (token + 1 < p.tokens) pos.load(p, token + 1);  // in time for the next token
     }
     if (at.is_k != tensor) {
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
           w[1].load(src + L.e1);
         }
       }
-      qk_turn_terms<VEC, INTER, NORM && !BWD>(ws, BWD ? -1.0f : 1.0f, w, P, Q);
+      qk_turn_terms<VEC, INTER, NORM && !BWD>(angles, L, BWD ? -1.0f : 1.0f, w, P, Q);
       if constexpr (BWD && NORM) {
 #pragma unroll
         for (int j = 0; j < H; ++j) acc[0][j] = acc[1][j] = 0;
