@@ -218,7 +218,8 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
  *
  *   A [h, 2 ffn] = [Ag | Au], a [2 ffn], GU [tokens, 2 ffn] = [G | U], dGU likewise,
  *   dA [h, 2 ffn], da [2 ffn]; the other shapes, types and constraints as for mlp_fwd
- *   (t must divide ffn, and ffn / t and h be multiples of 8; ffn <= 2^29).
+ *   (t must divide ffn, and ffn / t and h be multiples of 8; ffn <= 2^29, h and tokens
+ *   <= 2^30).
  *
  * glu_fwd: a and b may be NULL (no bias), R NULL means R = X.  GU [tokens, 2 ffn] is
  *   written for the backward and may be NULL; Y [tokens, ffn] is always written.

@@ -33,7 +33,8 @@ ATTN_BWD = dict(**ATTN, res=1, acc=1, **{k: GOOD for k in ("dOut X Wqkv Wo QKV Q
 EINVAL, EALIGN, EUNS = mlp.MLP_EINVAL, mlp.MLP_EALIGN, mlp.MLP_EUNSUPPORTED
 
 BAD_GLU = [(dict(h=0), EINVAL), (dict(h=12), EINVAL), (dict(ffn=0), EINVAL), (dict(ffn=252), EINVAL), (dict(t=0), EINVAL),
-           (dict(t=3), EINVAL), (dict(t=64), EINVAL), (dict(tokens=0), EINVAL), (dict(tokens=-1), EINVAL), (dict(tokens=1 << 31), EINVAL)]
+           (dict(t=3), EINVAL), (dict(t=64), EINVAL), (dict(tokens=0), EINVAL), (dict(tokens=-1), EINVAL), (dict(tokens=1 << 31), EINVAL), (dict(tokens=(1 << 30) + 1), EINVAL),
+           (dict(ffn=(1 << 29) + 8, t=1), EINVAL)]
 BAD_ACT = [(dict(act=2), EINVAL), (dict(act=-1), EINVAL), (dict(p=1.0), EINVAL), (dict(p=-0.5), EINVAL), (dict(p=float("nan")), EINVAL)]
 BAD_ROPE = [(dict(rot=0), EINVAL), (dict(rot=60), EINVAL), (dict(rot=72, s0=36), EINVAL), (dict(inter=2), EINVAL), (dict(axes=0), EINVAL),
             (dict(axes=4), EINVAL), (dict(s0=31), EINVAL), (dict(s0=33, s1=-1), EINVAL), (dict(s0=16, s1=16), EINVAL),

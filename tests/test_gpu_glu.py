@@ -348,6 +348,136 @@ def test_graph_replay_streams_and_repeats_give_the_same_bits(T):
     check_backward_input(c, b["GU"], b["dZ"], b["dGU"], b["dX"])
 
 
+@pytest.mark.parametrize("T,h,ffn", [(3, 264, 520), (300, 2056, 2056), (1300, 2568, 1288)])
+def test_without_dependent_launches_the_same_bits(T, h, ffn):
+    """With each launch waiting for the one before to end (mlp_set_dependent_launch(0)): no bit changes, so no
+    launch reads early what another still writes."""
+    c = Case(T, h, ffn, "silu", 0.1, True)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        GU, Y, O = torch.empty(T, 2 * ffn, **bf), torch.empty(T, ffn, **bf), torch.empty(T, h, **bf)
+        dZ, dGU, dX = torch.empty(T, h, **bf), torch.empty(T, 2 * ffn, **bf), torch.empty(T, h, **bf)
+        g = [torch.empty(s, device="cuda") for s in ((h, 2 * ffn), (2 * ffn,), (ffn, h), (h,))]
+        for _ in range(3):
+            c.fwd(GU, Y, O)
+            c.bwd_input(GU, dZ, dGU, dX)
+            c.bwd_weights(dZ, Y, dGU, *g)
+        _status_ok()
+        return [GU, Y, O, dZ, dGU, dX, *g]
+
+    first = step()
+    try:
+        mlp.mlp_set_dependent_launch(False)
+        second = step()
+    finally:
+        mlp.mlp_set_dependent_launch(True)
+    for k, (a, b) in enumerate(zip(first, second)):
+        assert torch.equal(a, b), k
+
+
+def test_weights_written_just_before_the_call():
+    """Weights that the launch right before the call writes (an optimizer step on the stream) are the ones used."""
+    T, h, ffn = 5, 1032, 2744
+    c = Case(T, h, ffn, "silu", 0.0, False)
+    other = Case(T, h, ffn, "silu", 0.0, False, seed=8)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    outs = []
+    for rounds in (1, 30):
+        Y, O = torch.empty(T, ffn, **bf), torch.empty(T, h, **bf)
+        for k in range(rounds):
+            src = other if k % 2 else c
+            c.X.copy_(c.X)
+            A, B = (src.A, src.B)
+            master = [x.float() for x in (A, B)]
+            m, v = [torch.zeros_like(x) for x in master], [torch.ones_like(x) for x in master]
+            wA, wB = torch.empty_like(A), torch.empty_like(B)
+            for w, g, mm, vv in ((wA, master[0], m[0], v[0]), (wB, master[1], m[1], v[1])):
+                mlp.adam_step(torch.zeros_like(g), g, mm, vv, w, lr=0.0)    # writes w = bf16(master)
+            mlp.glu_fwd(h, ffn, 1, T, 0.0, SEED, OFFSET, ACT["silu"], c.X, wA, None, wB, None, None, None, Y, O)
+            _status_ok()
+            outs.append((k % 2, Y.clone(), O.clone()))
+    for odd in (0, 1):
+        same = [(y, o) for k, y, o in outs if k == odd]
+        assert all(torch.equal(y, same[0][0]) and torch.equal(o, same[0][1]) for y, o in same)
+    check_forward(c, None, outs[0][1], outs[0][2])
+
+
+def test_threads_calling_at_once():
+    """Two host threads, a stream each, the kernels' one-time set-up among their calls' work: the bits of one thread."""
+    import threading
+    cs = [Case(40, 520, 1096, "gelu", 0.1, True, seed=s) for s in (1, 2)]
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    outs = [[torch.empty(40, n, **bf) for n in (2 * 1096, 1096, 520)] for _ in range(4)]
+    for c, o in zip(cs, outs):
+        c.fwd(*o)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(c, o):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    c.fwd(*o)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cs, outs[2:])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _status_ok()
+    assert not errors
+    for a, b in zip(outs[:2], outs[2:]):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+FRESH = """
+import sys
+sys.path.insert(0, "tests")
+import torch
+import test_gpu_glu as t, test_gpu_qk_rope as q
+from transformer_lm_megatron_gb300 import mlp
+mlp.load()
+for T in (3, 700):
+    c, r = t.Case(T, 1032, 1544, "silu", 0.1, True), q.Case(T, 4, 2, 128)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    GU, Y, O = torch.empty(T, 2 * 1544, **bf), torch.empty(T, 1544, **bf), torch.empty(T, 1032, **bf)
+    dZ, dGU, dX = torch.empty(T, 1032, **bf), torch.empty(T, 2 * 1544, **bf), torch.empty(T, 1032, **bf)
+    (Qo, _), (Ko, _), (dQ, _), (dK, _) = r.out(4), r.out(2), r.out(4), r.out(2)
+    w = r.grads()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        c.fwd(GU, Y, O)
+        c.bwd_input(GU, dZ, dGU, dX)
+        r.fwd(Qo, Ko)
+        r.bwd(dQ, dK, w)
+    g.replay()
+    t._status_ok()
+    t.check_forward(c, GU, Y, O)
+    t.check_backward_input(c, GU, dZ, dGU, dX)
+    q.check_fwd(r, Qo, Ko)
+    q.check_bwd(r, dQ, dK, w)
+print("captured first calls agree")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """A fresh process whose first calls are captured into a graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH], cwd=root, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0 and "agree" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
 def test_transposed_copies_change_no_bit():
     """scratch with mlp_set_wgrad_transpose(1): the weight gradients read transposed copies."""
     c = Case(1024, 1032, 1544, "silu")

@@ -58,11 +58,14 @@ int launch_few_tokens(DeviceState* st, const uint16_t* W, const uint16_t* X, Few
   if (!rc) rc = make_map(&mX, X, p.K, p.T, p.K, kBK, (uint32_t)p.tpad);
   if (rc) return rc;
   auto kern = k_few_tokens<KIND>;
-  bool& ready = st->few_attr[KIND];
-  if (!ready) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFtSmem + 1024);
-    if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (few tokens): %s", cudaGetErrorString(e));
-    ready = true;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    bool& ready = st->few_attr[KIND];
+    if (!ready) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFtSmem + 1024);
+      if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (few tokens): %s", cudaGetErrorString(e));
+      ready = true;
+    }
   }
   const int ts = trace_pre(s);
   const cudaError_t e = launch_kernel(kern, dim3((unsigned)(tiles * token_tiles * p.split)), dim3(kFtThreads),

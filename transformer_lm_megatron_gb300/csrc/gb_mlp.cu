@@ -127,6 +127,7 @@ struct DeviceState {
 
 
 std::mutex g_mu;
+std::mutex g_setup_mu;  // the one-time set-up of the gated block's and the head norms' kernels
 DeviceState g_dev[kMaxDevices];
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -140,6 +141,14 @@ int device_state(DeviceState** out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(MLP_EUNSUPPORTED, "no CUDA device: %s", cudaGetErrorString(e));
   if (dev < 0 || dev >= kMaxDevices) return fail(MLP_EUNSUPPORTED, "device ordinal %d out of range", dev);
+  // A host thread has no context until a runtime call binds one to it, and tensor maps are
+  // encoded by a driver call, which binds none.
+  thread_local int bound = -1;
+  if (bound != dev) {
+    e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return fail(MLP_EUNSUPPORTED, "device %d: %s", dev, cudaGetErrorString(e));
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& st = g_dev[dev];
   if (!st.ready) {
@@ -1092,7 +1101,9 @@ int qk_norm_rope_bwd(int64_t tokens, int nq, int nk, int d, int rot, int interle
 static int check_glu(const char* what, int h, int ffn, int t, int64_t tokens, float p) {
   const int rc = check_shape(h, ffn, t, -1, tokens, p);
   if (rc) return rc;
-  if (ffn > (1 << 29)) return fail(MLP_EINVAL, "%s: ffn = %d is too large", what, ffn);
+  // (row and column counts stay within int with a tile added, 2 ffn too)
+  if (ffn > (1 << 29) || h > (1 << 30) || tokens > (int64_t)1 << 30)
+    return fail(MLP_EINVAL, "%s: h = %d, ffn = %d or tokens = %lld is too large", what, h, ffn, (long long)tokens);
   return MLP_OK;
 }
 

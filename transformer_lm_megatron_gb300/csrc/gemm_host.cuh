@@ -299,6 +299,7 @@ int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
   *split = 0;
   if (g_pair_mode.load(std::memory_order_relaxed) == 0) return MLP_OK;
   auto kern = k_gemm_split<AM, BM, GATED>;
+  std::lock_guard<std::mutex> lock(g_setup_mu);
   int* clusters = st->split_clusters[(AM ? 2 : 0) + (BM ? 1 : 0) + 4 * GATED];
   if (clusters[kGsMaxSplit - 1] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGsSmemBytes);

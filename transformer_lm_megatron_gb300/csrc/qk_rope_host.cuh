@@ -82,15 +82,20 @@ template <int VEC, bool INTER, bool NORM, bool BWD>
 int launch_qk_t(DeviceState* st, QkRopeParams& p, cudaStream_t s, unsigned* ctas) {
   auto kern = k_qk_norm_rope<VEC, INTER, NORM, BWD>;
   constexpr int smem = QkSmem<VEC, BWD, NORM>::kBytes;
-  int& per_sm = st->qk_per_sm[(VEC == 8 ? 8 : 0) + (INTER ? 4 : 0) + (NORM ? 2 : 0) + (BWD ? 1 : 0)];
-  if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    int n = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kQkThreads, smem);
-    if (e != cudaSuccess || n < 1) return fail(MLP_ECUDA, "head norms and rotation: %s", cudaGetErrorString(e));
-    per_sm = n < kQkMaxPerSm ? n : kQkMaxPerSm;
+  int ctas_per_sm;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    int& per_sm = st->qk_per_sm[(VEC == 8 ? 8 : 0) + (INTER ? 4 : 0) + (NORM ? 2 : 0) + (BWD ? 1 : 0)];
+    if (per_sm == 0) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      int n = 0;
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kQkThreads, smem);
+      if (e != cudaSuccess || n < 1) return fail(MLP_ECUDA, "head norms and rotation: %s", cudaGetErrorString(e));
+      per_sm = n < kQkMaxPerSm ? n : kQkMaxPerSm;
+    }
+    ctas_per_sm = per_sm;
   }
-  *ctas = plan_qk_rope(st, &p, VEC, per_sm);
+  *ctas = plan_qk_rope(st, &p, VEC, ctas_per_sm);
   const int ts = trace_pre(s);
   const cudaError_t e = launch_kernel(kern, dim3(*ctas), dim3(kQkThreads), smem, s, 1, 1, p);
   trace_post(ts, s, BWD ? kTraceQkRopeBwd : kTraceQkRope, p.tokens, (int64_t)(p.nq + p.nk) * p.d, 0);
