@@ -101,25 +101,28 @@ __global__ void __launch_bounds__(kColThreads)
   }
 }
 
-// dZ = dO * keep * scale (rounded to bf16), 8 columns a thread step.  The gated block's
-// input gradient; its bias gradient is a column sum in the weight-gradient pass.
-__global__ void __launch_bounds__(256)
+// dZ = dO * keep * scale (rounded to bf16), 8 columns a thread step, a row of threads to a
+// row.  The gated block's input gradient; its bias gradient is a column sum in the
+// weight-gradient pass.
+constexpr int kDropThreads = 128;
+__global__ void __launch_bounds__(kDropThreads)
     k_dropout_bwd(const uint16_t* dO, uint16_t* dZ, int64_t rows, int cols, DropoutParams drop) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int per_row = cols / 8;
-  const int64_t n = rows * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i / per_row;
-    const uint32_t keep = dropout_keep8(drop, r, (i - r * per_row) * 8);
-    const uint4 q = reinterpret_cast<const uint4*>(dO)[i];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t o[4];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const uint4* in = reinterpret_cast<const uint4*>(dO + r * cols);
+    uint4* out = reinterpret_cast<uint4*>(dZ + r * cols);
+    for (int c = threadIdx.x; c < cols / 8; c += kDropThreads) {
+      const uint4 q = in[c];
+      const uint32_t keep = dropout_keep8(drop, r, 8 * c);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2((keep >> (2 * j)) & 1u ? bf16lo(w[j]) * drop.scale : 0.0f,
-                         (keep >> (2 * j + 1)) & 1u ? bf16hi(w[j]) * drop.scale : 0.0f);
-    reinterpret_cast<uint4*>(dZ)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int j = 0; j < 4; ++j)
+        o[j] = pack_bf16x2((keep >> (2 * j)) & 1u ? bf16lo(w[j]) * drop.scale : 0.0f,
+                           (keep >> (2 * j + 1)) & 1u ? bf16hi(w[j]) * drop.scale : 0.0f);
+      out[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -173,17 +176,18 @@ __global__ void __launch_bounds__(kColThreads)
 
 // The column sums of two contiguous matrices of as many rows, the gated block's da and db
 // in one launch (two launches took 14 us of 51 at 1317 tokens, h 1032, ffn 2744).  Either
-// may have no columns.  Grid (blocks of x0 + blocks of x1, split), clusters as above.
+// may have no columns.  late_wait as for k_gemm_bf16_tc.  Grid (blocks of x0 + blocks of x1, split), clusters as above.
 __global__ void __launch_bounds__(kColThreads)
     k_colsum_two(const uint16_t* x0, float* out0, int cols0, const uint16_t* x1, float* out1, int cols1, int64_t rows,
-                 int accumulate) {
-  grid_dependency_wait();
+                 int accumulate, int late_wait) {
+  if (!late_wait) grid_dependency_wait();
   grid_launch_dependents();
   const int blocks0 = (cols0 + kColsPerCta - 1) / kColsPerCta;
   const bool second = (int)blockIdx.x >= blocks0;
   const int cols = second ? cols1 : cols0;
   colsum_block(second ? x1 : x0, cols, second ? out1 : out0, rows, cols, (int)blockIdx.x - (second ? blocks0 : 0),
                accumulate);
+  if (late_wait) grid_dependency_wait();
 }
 
 // p[0 .. n) = 0 with 16-byte stores; n % 4 == 0 and p 16-byte aligned.

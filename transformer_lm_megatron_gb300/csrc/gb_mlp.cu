@@ -1187,11 +1187,10 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
   const int T = (int)tokens;
   const mlp_bf16* g = dO;  // without dropout dZ is dO
   if (p > 0.0f) {
-    const int64_t n = tokens * (h / 8);
-    const int64_t blocks = (n + 255) / 256 < (int64_t)st->sms * 8 ? (n + 255) / 256 : (int64_t)st->sms * 8;
+    const int64_t blocks = tokens < (int64_t)st->sms * 16 ? tokens : (int64_t)st->sms * 16;
     const int ts = trace_pre(s);
-    const cudaError_t e = launch_kernel(k_dropout_bwd, dim3((unsigned)blocks), dim3(256), 0, s, 1, 1, dO, dZ, tokens, h,
-                                        make_dropout(p, seed, token_offset, h));
+    const cudaError_t e = launch_kernel(k_dropout_bwd, dim3((unsigned)blocks), dim3(kDropThreads), 0, s, 1, 1, dO, dZ,
+                                        tokens, h, make_dropout(p, seed, token_offset, h));
     trace_post(ts, s, kTraceDropBwd, tokens, h, 0);
     rc = launch_check(e, "dropout backward");
     if (rc) return rc;
@@ -1241,20 +1240,6 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int T = (int)tokens, f2 = 2 * ffn, acc = accumulate ? 1 : 0;
-  // da and db; the products read nothing that this launch writes, so they need not wait
-  // for its end (late wait), and dB's need not wait for dA's
-  const bool sums = da != nullptr || db != nullptr;
-  if (sums) {
-    const int c0 = da != nullptr ? f2 : 0, c1 = db != nullptr ? h : 0;
-    const int blocks = (c0 + kColsPerCta - 1) / kColsPerCta + (c1 + kColsPerCta - 1) / kColsPerCta;
-    const unsigned split = colsum_split(st, (int64_t)blocks * kColsPerCta, k_colsum_two);
-    const int ts = trace_pre(s);
-    const cudaError_t e = launch_kernel(k_colsum_two, dim3((unsigned)blocks, split), dim3(kColThreads), 0, s, 1, split, dGU,
-                                        da, c0, dZ, db, c1, tokens, acc);
-    trace_post(ts, s, kTraceColsum, tokens, c0 + c1, 0);
-    rc = launch_check(e, "bias-gradient column sums");
-    if (rc) return rc;
-  }
   // transposed copies of X and dZ for large products, as in mlp_bwd
   const mlp_bf16* Xt = nullptr;
   const mlp_bf16* dZt = nullptr;
@@ -1271,14 +1256,26 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   ea.ld = f2;
   ea.g_out = dA;
   rc = Xt ? gemm_block<false, true>(st, Xt, T, dGU, f2, h, f2, T, ea, s, kTraceGluDW)
-          : gemm_block<true, true>(st, X, h, dGU, f2, h, f2, T, ea, s, kTraceGluDW, sums);
+          : gemm_block<true, true>(st, X, h, dGU, f2, h, f2, T, ea, s, kTraceGluDW);
   if (rc) return rc;
   EpiParams eb{};
   eb.kind = acc ? kEpiF32Add : kEpiF32Store;
   eb.ld = h;
   eb.g_out = dB;
-  return dZt ? gemm_block<true, false>(st, Y, ffn, dZt, T, ffn, h, T, eb, s, kTraceGluDW)
-             : gemm_block<true, true>(st, Y, ffn, dZ, h, ffn, h, T, eb, s, kTraceGluDW, true);
+  // (dB's product reads nothing that dA's writes, and the column sums nothing that either
+  // writes: each may begin while the one before ends)
+  rc = dZt ? gemm_block<true, false>(st, Y, ffn, dZt, T, ffn, h, T, eb, s, kTraceGluDW)
+           : gemm_block<true, true>(st, Y, ffn, dZ, h, ffn, h, T, eb, s, kTraceGluDW, true);
+  if (rc || (da == nullptr && db == nullptr)) return rc;
+  const int c0 = da != nullptr ? f2 : 0, c1 = db != nullptr ? h : 0;
+  const int blocks = (c0 + kColsPerCta - 1) / kColsPerCta + (c1 + kColsPerCta - 1) / kColsPerCta;
+  const unsigned split = colsum_split(st, (int64_t)blocks * kColsPerCta, k_colsum_two);
+  const int late = g_late_wait.load(std::memory_order_relaxed) ? 1 : 0;
+  const int ts = trace_pre(s);
+  const cudaError_t e = launch_kernel(k_colsum_two, dim3((unsigned)blocks, split), dim3(kColThreads), 0, s, 1, split, dGU, da,
+                                      c0, dZ, db, c1, tokens, acc, late);
+  trace_post(ts, s, kTraceColsum, tokens, c0 + c1, 0);
+  return launch_check(e, "bias-gradient column sums");
 }
 
 int mlp_sync_status(void* stream) {
