@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kFtThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (p.split > 1) cluster_arrive();
+  if (p.split > 1) cluster_arrive_relaxed();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 

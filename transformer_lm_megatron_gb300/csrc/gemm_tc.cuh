@@ -1144,7 +1144,7 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_empty[acc]), 0));
         else
           mbar_arrive(&acc_empty[acc]);
       }
@@ -1156,7 +1156,9 @@ __global__ void __launch_bounds__(GemmCfg<PAIR, BATCHED || WIDE>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // the even CTA's MMAs no longer read the odd CTA's smem / TMEM
+  // The even CTA's MMAs no longer read the odd CTA's smem / TMEM, and the arrivals that the odd
+  // one's warps sent to the even one's barriers have landed (so with a release).
+  if constexpr (PAIR) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem_base, kTmemCols);
