@@ -265,7 +265,7 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
  *   tokens in [1, 2^31), nq, nk >= 1 heads of queries and keys; d a multiple of 8, at
  *   most 256; rot a multiple of 8, 8 <= rot <= d; eps >= 0.
  *   wq, wk [d] bf16 or both NULL; pos [n_axes, tokens] int32 (any value, negative ones
- *   too); inv_freq [rot/2] fp32, radians per position.
+ *   too); inv_freq [rot/2] fp32, finite, in radians per position.
  *   Q, K, Qo, Ko, and in the backward dQo, dKo (gradients of Qo, Ko), dQ, dK:
  *   [tokens, heads, d] bf16, 16-byte aligned, a token's heads side by side, rows ld
  *   elements apart (a multiple of 8, at least heads * d): the queries and keys inside a

@@ -10,13 +10,13 @@ constexpr int kFtSmem = 110 * 1024;
 // beyond while the weights, read from L2 once for each 64 tokens, stay under a limit: for a
 // pass's first product (G, U and the gate, or dG and dU) of up to 512 tokens 64 MB, for its
 // second (O, or dX) 96 MB.  Measured, few-token / GEMM (us of a pass, the other product alike):
-//   both   48 tokens, h 4096, ffn 16384 68 / 79; h 2048, ffn 5464 21 / 36
-//   first  200 tokens, h 1024, ffn 4096 19 / 22; 192 tokens, h 2048, ffn 5464 34 / 31; 1600
-//          tokens, h 640, ffn 1280 25 / 21; backward: 256 tokens, h 1024, ffn 4096 23 / 28, h
-//          376, ffn 4752 19 / 23; 1024 tokens, h 376, ffn 4752 49 / 39
-//   second 400 tokens, h 1024, ffn 4096 25 / 30; 192 tokens, h 4096, ffn 16384 108 / 91; 1600
-//          tokens, h 1032, ffn 2744 55 / 47; backward: 128 tokens, h 2048, ffn 5464 29 / 38;
-//          512 tokens, h 376, ffn 4752 25 / 34; 1024 tokens, h 1024, ffn 4096 55 / 42
+//   both   48 tokens, h 4096, ffn 16384 66 / 77; h 2048, ffn 5464 21 / 36
+//   first  200 tokens, h 1024, ffn 4096 18 / 21; 192 tokens, h 2048, ffn 5464 34 / 31; 1600
+//          tokens, h 640, ffn 1280 24 / 19; backward: 256 tokens, h 1024, ffn 4096 22 / 25, h
+//          376, ffn 4752 17 / 20; 1024 tokens, h 376, ffn 4752 47 / 37
+//   second 400 tokens, h 1024, ffn 4096 23 / 29; 192 tokens, h 4096, ffn 16384 109 / 92; 1600
+//          tokens, h 1032, ffn 2744 53 / 44; backward: 128 tokens, h 2048, ffn 5464 28 / 37;
+//          512 tokens, h 376, ffn 4752 24 / 34; 1024 tokens, h 1024, ffn 4096 43 / 40
 bool few_tokens_first(int T, int64_t weight_bytes) {
   return T <= 64 || (T <= 512 && (T + 63) / 64 * weight_bytes <= 64ll << 20);
 }
@@ -35,8 +35,8 @@ int launch_few_tokens(DeviceState* st, const uint16_t* W, const uint16_t* X, Few
   // CTAs share a tile's reduction until two to an SM are at work, each with 4 k-blocks or
   // more.  A stage is 16 KB of weights and 128 bytes a token; two CTAs share an SM's 227 KB,
   // with three stages each or more beside what they are sent (a CTA by itself leaves its
-  // sums in its own ring).  27 tokens at h 2048, ffn 5464: 19 us; with CTAs for 1.25 or 1.5
-  // to an SM 20 us, with three small CTAs to an SM 32 us (two stages each).
+  // sums in its own ring).  27 tokens at h 2048, ffn 5464: 18 us; with CTAs for 1.25 or 1.5
+  // to an SM 1 us more, with three small CTAs to an SM (two stages each) 13 us more.
   const int rows = p.T < p.tpad ? p.T : p.tpad, stage_bytes = (int)kFtWBytes + p.tpad * kBK * 2;
   int64_t split = 2 * (int64_t)st->sms / ((int64_t)tiles * token_tiles);
   if (split > num_kb / 4) split = num_kb / 4;

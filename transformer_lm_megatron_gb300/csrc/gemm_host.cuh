@@ -283,17 +283,19 @@ int make_half_map(CUtensorMap* m, const uint16_t* base, int64_t half_cols, int64
 }
 
 // Whether a GEMM of the gated block is of two waves of tiles or less of under 64 k-blocks
-// each, where 8 epilogue warps pay (1317 tokens, h 1032, ffn 2744 forward: 54 us with 4, 49
-// us with 8; 2048 tokens, h 4096, ffn 16384, with 256 k-blocks: 486 and 498 us).  `cols`
-// counts the MMA's columns.
+// each, where 8 epilogue warps pay (input gradient of 1317 tokens, h 1032, ffn 2744: 41.1 us
+// with 4, 39.9 with 8; forward of 2048 tokens, h 4096, ffn 16384, with 256 k-blocks: 493 and
+// 504 us).  `cols` counts the MMA's columns.
 bool few_waves(const DeviceState* st, int M, int64_t cols, int K) {
   return (K + kBK - 1) / kBK < 64 && (int64_t)((M + 2 * kBM - 1) / (2 * kBM)) * ((cols + kBN - 1) / kBN) <= 2 * (st->sms / 2);
 }
 
 // The pairs to share one tile's reduction among (k_gemm_split), or 0 where the tiles fill
-// the SMs by themselves.  Each pair has 6 k-blocks or more, as many as its ring holds.  (One
-// pair to a tile there is no faster than the persistent kernel: 42 and 40 us for the input
-// gradient at 1024 tokens, h 1024, ffn 4096.)
+// the SMs by themselves.  Each pair has 6 k-blocks or more, as many as its ring holds.
+// Persistent kernel and this (us of a pass): input gradient of 1317 tokens, h 1032, ffn 2744
+// 53 and 40, of 1024 tokens, h 1024, ffn 4096 63 and 40; forward 47 and 40, and of 3000 tokens,
+// h 768, ffn 2048 38 and 35.  (One pair to a tile here is no faster than there: 42 and 40 us
+// for that second input gradient.)
 template <bool AM, bool BM, int GATED>
 int split_pairs(DeviceState* st, int M, int64_t cols, int K, int* split) {
   *split = 0;
