@@ -101,28 +101,38 @@ __global__ void __launch_bounds__(kColThreads)
   }
 }
 
-// dZ = dO * keep * scale (rounded to bf16), 8 columns a thread step, a row of threads to a
-// row.  The gated block's input gradient; its bias gradient is a column sum in the
-// weight-gradient pass.
+// dZ = dO * keep * scale (rounded to bf16), 8 columns a thread step; which elements a
+// thread's first step keeps is worked out ahead of the wait for the kernel before.  The
+// gated block's input gradient; its bias gradient is a column sum in the weight-gradient
+// pass.
 constexpr int kDropThreads = 128;
 __global__ void __launch_bounds__(kDropThreads)
     k_dropout_bwd(const uint16_t* dO, uint16_t* dZ, int64_t rows, int cols, DropoutParams drop) {
+  const int64_t step = (int64_t)gridDim.x * kDropThreads;
+  const int per_row = cols / 8, step_c = (int)(step % per_row);
+  const int64_t step_r = step / per_row;
+  int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x, r = i / per_row;
+  int c = (int)(i - r * per_row);
+  uint32_t keep = r < rows ? dropout_keep8(drop, r, 8 * c) : 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const uint4* in = reinterpret_cast<const uint4*>(dO + r * cols);
-    uint4* out = reinterpret_cast<uint4*>(dZ + r * cols);
-    for (int c = threadIdx.x; c < cols / 8; c += kDropThreads) {
-      const uint4 q = in[c];
-      const uint32_t keep = dropout_keep8(drop, r, 8 * c);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      uint32_t o[4];
+  while (r < rows) {
+    const uint4 q = reinterpret_cast<const uint4*>(dO)[i];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = pack_bf16x2((keep >> (2 * j)) & 1u ? bf16lo(w[j]) * drop.scale : 0.0f,
-                           (keep >> (2 * j + 1)) & 1u ? bf16hi(w[j]) * drop.scale : 0.0f);
-      out[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 4; ++j)
+      o[j] = pack_bf16x2((keep >> (2 * j)) & 1u ? bf16lo(w[j]) * drop.scale : 0.0f,
+                         (keep >> (2 * j + 1)) & 1u ? bf16hi(w[j]) * drop.scale : 0.0f);
+    reinterpret_cast<uint4*>(dZ)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    i += step;
+    r += step_r;
+    c += step_c;
+    if (c >= per_row) {
+      c -= per_row;
+      ++r;
     }
+    if (r < rows) keep = dropout_keep8(drop, r, 8 * c);
   }
 }
 

@@ -1187,7 +1187,8 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
   const int T = (int)tokens;
   const mlp_bf16* g = dO;  // without dropout dZ is dO
   if (p > 0.0f) {
-    const int64_t blocks = tokens < (int64_t)st->sms * 16 ? tokens : (int64_t)st->sms * 16;
+    const int64_t steps = tokens * (h / 8), ctas = (steps + kDropThreads - 1) / kDropThreads;
+    const int64_t blocks = ctas < (int64_t)st->sms * 16 ? ctas : (int64_t)st->sms * 16;
     const int ts = trace_pre(s);
     const cudaError_t e = launch_kernel(k_dropout_bwd, dim3((unsigned)blocks), dim3(kDropThreads), 0, s, 1, 1, dO, dZ,
                                         tokens, h, make_dropout(p, seed, token_offset, h));
