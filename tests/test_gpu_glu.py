@@ -16,6 +16,7 @@ import pytest
 import torch
 
 from oracle import glu_oracle as glo
+from oracle import mlp_oracle
 from transformer_lm_megatron_gb300 import build as gb_build
 from transformer_lm_megatron_gb300 import mlp
 
@@ -374,6 +375,22 @@ def test_without_dependent_launches_the_same_bits(T, h, ffn):
         mlp.mlp_set_dependent_launch(True)
     for k, (a, b) in enumerate(zip(first, second)):
         assert torch.equal(a, b), k
+
+
+# more elements than dropout's backward has threads (152 SMs * 16 CTAs * 128 threads * 8), so that its
+# threads step on: over rows, over parts of rows, over rows of a single step
+@pytest.mark.parametrize("T,h", [(3001, 1032), (1500, 5208), (330001, 8)])
+def test_dropout_backward_of_many_elements(T, h):
+    c = Case(T, h, 8)
+    assert T * h > 152 * 16 * 128 * 8
+    GU = torch.randn(T, 16, device="cuda").to(torch.bfloat16)
+    (dZ, behind), dGU, dX = _guarded(T, h), torch.empty_like(GU), torch.empty_like(c.X)
+    c.bwd_input(GU, dZ, dGU, dX)
+    _status_ok()
+    ref = f64(c.dO) * mlp_oracle.dropout_keep(T, h, c.p, SEED, OFFSET) * mlp_oracle.dropout_scale(c.p)
+    # the scale and the product are each rounded to fp32 (2^-24), the result to bf16 (2^-8 of it)
+    assert np.all(np.abs(f64(dZ) - ref) <= np.abs(ref) * (BF + 2.0**-22))
+    assert torch.all(behind == 7)
 
 
 def test_weights_written_just_before_the_call():
