@@ -263,7 +263,8 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
  * pairs turn with axis 0, the next s1 with axis 1, the next s2 with axis 2;
  * s0 + s1 + s2 = rot / 2, and sections of axes that are not there are 0.
  *   tokens in [1, 2^31), nq, nk >= 1 heads of queries and keys; d a multiple of 8, at
- *   most 256; rot a multiple of 8, 8 <= rot <= d; eps >= 0.
+ *   most 256; rot a multiple of 8, 8 <= rot <= d; eps >= 0 (at eps = 0 a head of all
+ *   zeros, which then has no norm, gives NaN: its outputs, its gradient, dwq or dwk).
  *   wq, wk [d] bf16 or both NULL; pos [n_axes, tokens] int32 (any value, negative ones
  *   too); inv_freq [rot/2] fp32, finite, in radians per position.
  *   Q, K, Qo, Ko, and in the backward dQo, dKo (gradients of Qo, Ko), dQ, dK:

@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
             ss[v] = f2_fma(xv, xv, ss[v]);
             sg[v] = f2_fma(f2_mul(y[v][j], w[v].pair(j)), xv, sg[v]);
           }
-        const float r = rsqrtf(fmaf(L.sum(f2_sum(ss[0]) + f2_sum(ss[1])), inv_d, p.eps));
+        // (a lane without a head has zeros, whose root at eps = 0 would put NaN into dw: it takes eps = 1)
+        const float r = rsqrtf(fmaf(L.sum(f2_sum(ss[0]) + f2_sum(ss[1])), inv_d, at.room > 0 ? p.eps : 1.0f));
         const float c = L.sum(f2_sum(sg[0]) + f2_sum(sg[1])) * inv_d * r * r * r;
         const uint64_t rr = f2(r, r), nc = f2(-c, -c);
 #pragma unroll
