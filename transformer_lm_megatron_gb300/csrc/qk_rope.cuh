@@ -283,9 +283,22 @@ __device__ __forceinline__ void qk_turn_terms(const QkAngles& angles, const QkLa
     }
 }
 
+// turns: whether the lane's elements turn at all.  Those behind `rot` take their weights alone,
+// since an infinity times the sine 0 of their pair would be NaN (a lane turns whole or not, and
+// where rot = d all do).
 template <int VEC, bool INTER, bool WEIGHTS>
 __device__ __forceinline__ void qk_turn(uint64_t (&x)[2][VEC / 2], const uint64_t (&P)[2][VEC / 2],
-                                        const uint64_t (&Q)[2][VEC / 2]) {
+                                        const uint64_t (&Q)[2][VEC / 2], bool turns) {
+  if (!turns) {
+    if constexpr (WEIGHTS) {
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) {
+        x[0][j] = f2_mul(x[0][j], P[0][j]);
+        x[1][j] = f2_mul(x[1][j], P[1][j]);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < VEC / 2; ++j) {
     const uint64_t a = x[0][j], b = x[1][j];
@@ -461,9 +474,9 @@ __global__ void __launch_bounds__(kQkThreads, 2) k_qk_norm_rope(QkRopeParams p) 
           y[1][j] = f2_mul(y[1][j], rr);
         }
       }
-      qk_turn<VEC, INTER, NORM>(y, P, Q);
+      qk_turn<VEC, INTER, NORM>(y, P, Q, L.turns);
     } else {
-      qk_turn<VEC, INTER, false>(y, P, Q);
+      qk_turn<VEC, INTER, false>(y, P, Q, L.turns);
       if constexpr (NORM) {
         // x stays packed: unpacked twice it costs fewer registers than it takes
         QkVec<VEC> x[2];
