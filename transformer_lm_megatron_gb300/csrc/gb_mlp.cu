@@ -122,12 +122,13 @@ struct DeviceState {
   int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 2) CTAs; last: set up
   bool few_attr[4] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
+  int colsum_per_sm[2] = {};  // per column-sum kernel (ColsumKernel): co-resident CTAs on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
 
 
 std::mutex g_mu;
-std::mutex g_setup_mu;  // the one-time set-up of the gated block's and the head norms' kernels
+std::mutex g_setup_mu;  // DeviceState's fields that a kernel's first launch fills in
 DeviceState g_dev[kMaxDevices];
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -272,16 +273,19 @@ int check_ptrs(const char* what, std::initializer_list<const void*> ptrs) {
   return MLP_OK;
 }
 
+enum ColsumKernel { kColsumOne = 0, kColsumTwo = 1 };  // k_colsum_bf16, k_colsum_two
+
 // CTAs per column block of the (memory-bound) column sum: the most (1, 2, 4 or 8)
 // for which the whole grid is resident at once (a second, partial wave would take
 // as long as the first); the choice depends on the shape and the device only, so
 // the summation order, and the result, is fixed for a shape.
 template <typename Kernel>
-unsigned colsum_split(const DeviceState* st, int64_t cols, Kernel kernel) {
-  static int per_sm = 0;  // per kernel (each kernel has its own signature, hence instantiation)
-  if (per_sm == 0) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kColThreads, 0) != cudaSuccess || n < 1) {
+unsigned colsum_split(DeviceState* st, int64_t cols, Kernel kernel, ColsumKernel which) {
+  int per_sm;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    int& n = st->colsum_per_sm[which];
+    if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kColThreads, 0) != cudaSuccess || n < 1)) {
       cudaGetLastError();
       n = 1;
     }
@@ -485,7 +489,7 @@ int mlp_bwd(int h, int ffn, int t, int slice, int64_t tokens, float p, uint64_t 
     if (rc) return rc;
     // da_i += sum_tok dU_i
     const int ts = trace_pre(s);
-    const unsigned split = colsum_split(st, f, k_colsum_bf16);
+    const unsigned split = colsum_split(st, f, k_colsum_bf16, kColsumOne);
     const cudaError_t e = launch_kernel(k_colsum_bf16, dim3((f + kColsPerCta - 1) / kColsPerCta, split),
                                         dim3(kColThreads), 0, s, 1, split, (const uint16_t*)(dU + c),
                                         (int64_t)ffn, da + c, tokens, f, accumulate ? 1 : 0);
@@ -611,11 +615,14 @@ int attn_core_fused(DeviceState* st, const QkSource& qk, const uint16_t* QKV, ui
     rc = make_map4(&mO, bf, 2, O, d, L, h, nh, d, ns, (int64_t)L * h, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
   if (rc) return rc;
-  if (!st->fa_attr) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_attn_fwd_fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFaSmemBytes);
-    if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (fused attention): %s", cudaGetErrorString(e));
-    st->fa_attr = true;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    if (!st->fa_attr) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(k_attn_fwd_fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFaSmemBytes);
+      if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute (fused attention): %s", cudaGetErrorString(e));
+      st->fa_attr = true;
+    }
   }
   const int64_t items = (int64_t)((L + kFaTile - 1) / kFaTile) * nh * ns;
   const unsigned grid = (unsigned)(items < st->sms ? items : st->sms);
@@ -670,12 +677,15 @@ int attn_core_bwd_fused(DeviceState* st, const QkSource& qk, const uint16_t* QKV
                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MLP_ECUDA, "cuTensorMapEncodeTiled (softmax-gradient row sums) failed (%d)", (int)r);
   }
-  if (!st->fb_attr) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_attn_bwd_fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFbSmemBytes);
-    if (e != cudaSuccess)
-      return fail(MLP_ECUDA, "cudaFuncSetAttribute (fused attention backward): %s", cudaGetErrorString(e));
-    st->fb_attr = true;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    if (!st->fb_attr) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(k_attn_bwd_fused, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFbSmemBytes);
+      if (e != cudaSuccess)
+        return fail(MLP_ECUDA, "cudaFuncSetAttribute (fused attention backward): %s", cudaGetErrorString(e));
+      st->fb_attr = true;
+    }
   }
   const int64_t items = (int64_t)((L + kFaTile - 1) / kFaTile) * nh * ns;
   const unsigned grid = (unsigned)(items < st->sms ? items : st->sms);
@@ -976,11 +986,10 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   // dbqkv (+)= sum dQKV; dWqkv (+)= X^T dQKV; dX = [dOut +] dQKV Wqkv^T
   {
     const int ts = trace_pre(s);
-    const cudaError_t e =
-        launch_kernel(k_colsum_bf16, dim3((unsigned)((h3 + kColsPerCta - 1) / kColsPerCta), colsum_split(st, h3, k_colsum_bf16)),
-                      dim3(kColThreads), 0, s, 1, colsum_split(st, h3, k_colsum_bf16), (const uint16_t*)dQKV, (int64_t)h3, dbqkv,
-                      tokens,
-                      (int)h3, acc);
+    const unsigned split = colsum_split(st, h3, k_colsum_bf16, kColsumOne);
+    const cudaError_t e = launch_kernel(k_colsum_bf16, dim3((unsigned)((h3 + kColsPerCta - 1) / kColsPerCta), split),
+                                        dim3(kColThreads), 0, s, 1, split, (const uint16_t*)dQKV, (int64_t)h3, dbqkv,
+                                        tokens, (int)h3, acc);
     trace_post(ts, s, kTraceColsum, tokens, h3, 0);
     rc = launch_check(e, "bias-gradient column sum");
     if (rc) return rc;
@@ -1270,7 +1279,7 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
   if (rc || (da == nullptr && db == nullptr)) return rc;
   const int c0 = da != nullptr ? f2 : 0, c1 = db != nullptr ? h : 0;
   const int blocks = (c0 + kColsPerCta - 1) / kColsPerCta + (c1 + kColsPerCta - 1) / kColsPerCta;
-  const unsigned split = colsum_split(st, (int64_t)blocks * kColsPerCta, k_colsum_two);
+  const unsigned split = colsum_split(st, (int64_t)blocks * kColsPerCta, k_colsum_two, kColsumTwo);
   const int late = g_late_wait.load(std::memory_order_relaxed) ? 1 : 0;
   const int ts = trace_pre(s);
   const cudaError_t e = launch_kernel(k_colsum_two, dim3((unsigned)blocks, split), dim3(kColThreads), 0, s, 1, split, dGU, da,

@@ -106,31 +106,36 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
   const int slot =
       (AM ? 2 : 0) + (BM ? 1 : 0) + (PAIR ? 4 : 0) + (BATCHED ? 8 : 0) + (WIDE ? 16 : 0) + 32 * GATED;
   constexpr int kTileN = GATED == kGatedFwd ? kBN / 2 : kBN;
-  if (!st->gemm_attr[slot]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmemBytes);
-    if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    if (PAIR) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
-      cudaLaunchConfig_t qc = {};
-      qc.gridDim = dim3(2 * (unsigned)st->sms, 1, 1);
-      qc.blockDim = dim3(Cfg::kThreads, 1, 1);
-      qc.dynamicSmemBytes = Cfg::kSmemBytes;
-      cudaLaunchAttribute qa[1];
-      qa[0].id = cudaLaunchAttributeClusterDimension;
-      qa[0].val.clusterDim.x = 2;
-      qa[0].val.clusterDim.y = 1;
-      qa[0].val.clusterDim.z = 1;
-      qc.attrs = qa;
-      qc.numAttrs = 1;
-      int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, kern, &qc);
-      if (e != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = st->sms / 2;
+  int max_pairs;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    if (!st->gemm_attr[slot]) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmemBytes);
+      if (e != cudaSuccess) return fail(MLP_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      if (PAIR) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
+        cudaLaunchConfig_t qc = {};
+        qc.gridDim = dim3(2 * (unsigned)st->sms, 1, 1);
+        qc.blockDim = dim3(Cfg::kThreads, 1, 1);
+        qc.dynamicSmemBytes = Cfg::kSmemBytes;
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = 2;
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        qc.attrs = qa;
+        qc.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &qc);
+        if (e != cudaSuccess || n <= 0) {
+          cudaGetLastError();
+          n = st->sms / 2;
+        }
+        st->max_pairs[slot] = n;
       }
-      st->max_pairs[slot] = n;
+      st->gemm_attr[slot] = true;
     }
-    st->gemm_attr[slot] = true;
+    max_pairs = st->max_pairs[slot];
   }
   const int64_t tiles = (int64_t)((M + Cfg::kTileM - 1) / Cfg::kTileM) * ((N + kTileN - 1) / kTileN) * batch;
   EpiParams epx = ep;
@@ -142,7 +147,7 @@ int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB,
   // Only for bf16 epilogues of plain GEMMs with a reduction of 16 k-blocks or more,
   // and never in a late-waiting launch: the workspace region is shared by all
   // launches on the stream, which therefore must not overlap while they use it.
-  const int units = PAIR ? st->max_pairs[slot] : st->sms;
+  const int units = PAIR ? max_pairs : st->sms;
   epx.split_base = (int)tiles;
   epx.split_ws = nullptr;
   epx.split_flags = nullptr;
