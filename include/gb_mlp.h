@@ -43,6 +43,10 @@
  *     and runs asynchronously.  A nonzero return means nothing was enqueued,
  *     except MLP_ECUDA, which reports a failed launch (later launches of the same
  *     call are not attempted).  mlp_last_error() describes the failure.
+ *   - The regions of that memory go by the stream of a call.  A graph keeps the region
+ *     of the stream that it was captured on: graphs of mlp_fwd, mlp_bwd, attn_fwd or
+ *     attn_bwd captured on one stream must not run at once, nor beside calls on that
+ *     stream.  (The other entry points have no such limit.)
  *   - Constraints: h > 0, h % 8 == 0; ffn % t == 0, f = ffn/t, f % 8 == 0;
  *     0 < tokens < 2^31; 0 <= p < 1; -1 <= slice < t.
  *   - A kernel that detects a broken pipeline (a bounded wait that ran out)
@@ -300,6 +304,10 @@ int qk_norm_rope_bwd(int64_t tokens, int nq, int nk, int d, int rot, int interle
  * QKr [tokens, 2h] bf16 holds [Qr | Kr] (written by the forward, read by the backward);
  * QKV holds the projection itself.  dwq, dwk and ws as for qk_norm_rope_bwd.  The other
  * arguments are those of attn_fwd / attn_bwd and qk_norm_rope_fwd.
+ * Captured into a graph these calls use none of the library's static device memory but
+ * the status word, so that graphs captured on one stream may run at once on others; the
+ * results then differ from the eager call's by fp32 summation order where that one
+ * splits its tail (mlp_set_split_tail).
  * Returns MLP_OK or an error code.
  */
 int attn_rope_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,

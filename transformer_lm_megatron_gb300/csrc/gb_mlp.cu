@@ -749,6 +749,17 @@ int adam_step(int64_t n, const float* grad, float grad_scale, float* master, flo
   return launch_check(e, "adam_step");
 }
 
+// Whether work on `s` is being captured into a graph, or cannot be told (the legacy stream
+// while another is captured).
+static bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &status) != cudaSuccess) {
+    cudaGetLastError();
+    return true;
+  }
+  return status != cudaStreamCaptureStatusNone;
+}
+
 // rope: null for attn_fwd; attn_rope_fwd's norms and rotation of the queries and keys,
 // which go to QKr [tokens, 2h] and are read by the core from there.
 static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr, int h, int nh, int t, int64_t tokens,
@@ -770,6 +781,7 @@ static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr
   rc = device_state(&st);
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool static_ws = rope == nullptr || !capturing(s);
   if (R == nullptr) R = X;
   const int T = (int)tokens, d = h / nh, L = seq_len, ns = T / L;
   const int64_t h3 = 3 * (int64_t)h, LL = (int64_t)L * L;
@@ -779,7 +791,7 @@ static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr
   e.ld = h3;
   e.out0 = QKV;
   e.bias = bqkv;
-  rc = gemm(st, X, false, h, Wqkv, true, h3, T, (int)h3, h, e, s, kTraceAttnGemm);
+  rc = gemm(st, X, false, h, Wqkv, true, h3, T, (int)h3, h, e, s, kTraceAttnGemm, false, static_ws);
   if (rc) return rc;
   QkSource qk{QKV, QKV + h, h3};
   if (rope != nullptr) {
@@ -806,14 +818,14 @@ static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr
     ezf.bias = bo;
     ezf.out0 = out;
     ezf.drop = make_dropout(p, seed, token_offset, h);
-    return gemm(st, O, false, h, Wo, true, h, T, h, h, ezf, s, kTraceAttnGemm);
+    return gemm(st, O, false, h, Wo, true, h, T, h, h, ezf, s, kTraceAttnGemm, false, static_ws);
   }
   // S = Q K^T / sqrt(d), -inf above the diagonal; per (sequence, head)
   EpiParams es{};
   es.kind = kEpiScaleMask;
   es.alpha = 1.0f / std::sqrt((float)d);
   rc = gemm_batched(st, {qk.q, false, L, d, qk.ld, d, L * qk.ld}, {qk.k, false, L, d, qk.ld, d, L * qk.ld},
-                    {S, L, L, L, LL, nh * LL}, L, L, d, nh, ns, es, s, kTraceAttnGemm, kCausalSkipUpper);
+                    {S, L, L, L, LL, nh * LL}, L, L, d, nh, ns, es, s, kTraceAttnGemm, kCausalSkipUpper, static_ws);
   if (rc) return rc;
   rc = softmax_launch(st, S, P, (int64_t)ns * nh * L, L, s);
   if (rc) return rc;
@@ -821,7 +833,7 @@ static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr
   EpiParams eo{};
   eo.kind = kEpiStore;
   rc = gemm_batched(st, {P, false, L, L, L, LL, nh * LL}, {QKV + 2 * h, true, d, L, h3, d, L * h3},
-                    {O, d, L, h, d, (int64_t)L * h}, L, d, L, nh, ns, eo, s, kTraceAttnGemm, kCausalKUpTo);
+                    {O, d, L, h, d, (int64_t)L * h}, L, d, L, nh, ns, eo, s, kTraceAttnGemm, kCausalKUpTo, static_ws);
   if (rc) return rc;
   // out = R + dropout(O Wo + bo): the row split of Wo summed over slices in the accumulator
   EpiParams ez{};
@@ -831,7 +843,7 @@ static int attn_fwd_impl(const char* what, const QkRopeArgs* rope, mlp_bf16* QKr
   ez.bias = bo;
   ez.out0 = out;
   ez.drop = make_dropout(p, seed, token_offset, h);
-  return gemm(st, O, false, h, Wo, true, h, T, h, h, ez, s, kTraceAttnGemm);
+  return gemm(st, O, false, h, Wo, true, h, T, h, h, ez, s, kTraceAttnGemm, false, static_ws);
 }
 
 int attn_fwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,
@@ -875,6 +887,7 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   rc = device_state(&st);
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool static_ws = rope == nullptr || !capturing(s);
   const int T = (int)tokens, d = h / nh, L = seq_len, ns = T / L;
   const int64_t h3 = 3 * (int64_t)h, LL = (int64_t)L * L;
   const int acc = accumulate ? 1 : 0;
@@ -902,9 +915,9 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   if (ds_holds_copy && wgrad_transposed(h, h, tokens, dS)) {
     rc = launch_transposes(s, tokens, h, TransposeJob{dZ, dS}, TransposeJob{nullptr, nullptr}, "transposed copy of dZ");
     if (rc) return rc;
-    rc = gemm(st, O, true, h, dS, false, T, h, h, T, ew, s, kTraceAttnGemm);
+    rc = gemm(st, O, true, h, dS, false, T, h, h, T, ew, s, kTraceAttnGemm, false, static_ws);
   } else {
-    rc = gemm(st, O, true, h, dZ, true, h, h, h, T, ew, s, kTraceAttnGemm);
+    rc = gemm(st, O, true, h, dZ, true, h, h, h, T, ew, s, kTraceAttnGemm, false, static_ws);
   }
   if (rc) return rc;
   // dO = dZ Wo^T
@@ -912,7 +925,7 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   ed.kind = kEpiStore;
   ed.ld = h;
   ed.out0 = dO;
-  rc = gemm(st, dZ, false, h, Wo, false, h, T, h, h, ed, s, kTraceAttnGemm);
+  rc = gemm(st, dZ, false, h, Wo, false, h, T, h, h, ed, s, kTraceAttnGemm, false, static_ws);
   if (rc) return rc;
   EpiParams est{};
   est.kind = kEpiStore;
@@ -934,13 +947,13 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
     rc = attn_core_bwd_fused(st, qk, QKV, P, dO, delta, dS, dQKV, h, nh, L, ns, s);
     if (rc) return rc;
     rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {qk.k, true, d, L, qk.ld, d, L * qk.ld},
-                      {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo);
+                      {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo, static_ws);
     if (rc) return rc;
   } else {
   // per (sequence, head): dV = P^T dO, dS = P (dO V^T - delta) / sqrt(d) with delta = rowsum(dO * O)
   // (fused: the product dO V^T never leaves the GEMM), dQ = dS K, dK = dS^T Q
   rc = gemm_batched(st, {P, true, L, L, L, LL, nh * LL}, {dO, true, d, L, h, d, (int64_t)L * h},
-                    {dQKV + 2 * h, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKFrom);
+                    {dQKV + 2 * h, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKFrom, static_ws);
   if (rc) return rc;
   float* delta = dP;  // ns * nh * L floats of the fp32 workspace
   {
@@ -961,13 +974,13 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   eg.ld = L;
   eg.alpha = 1.0f / std::sqrt((float)d);
   rc = gemm_batched(st, {dO, false, L, d, h, d, (int64_t)L * h}, {QKV + 2 * h, false, L, d, h3, d, L * h3},
-                    {dS, L, L, L, LL, nh * LL}, L, L, d, nh, ns, eg, s, kTraceAttnGemm, kCausalSkipUpper);
+                    {dS, L, L, L, LL, nh * LL}, L, L, d, nh, ns, eg, s, kTraceAttnGemm, kCausalSkipUpper, static_ws);
   if (rc) return rc;
   rc = gemm_batched(st, {dS, false, L, L, L, LL, nh * LL}, {qk.k, true, d, L, qk.ld, d, L * qk.ld},
-                    {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo);
+                    {dQKV, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKUpTo, static_ws);
   if (rc) return rc;
   rc = gemm_batched(st, {dS, true, L, L, L, LL, nh * LL}, {qk.q, true, d, L, qk.ld, d, L * qk.ld},
-                    {dQKV + h, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKFrom);
+                    {dQKV + h, d, L, h3, d, L * h3}, L, d, L, nh, ns, est, s, kTraceAttnGemm, kCausalKFrom, static_ws);
   if (rc) return rc;
   }
   if (rope != nullptr) {
@@ -1003,9 +1016,9 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   if (ds_holds_copy && wgrad_transposed(h, (int)h3, tokens, dS)) {
     rc = launch_transposes(s, tokens, h, TransposeJob{X, dS}, TransposeJob{nullptr, nullptr}, "transposed copy of X");
     if (rc) return rc;
-    rc = gemm(st, dS, false, T, dQKV, true, h3, h, (int)h3, T, eq, s, kTraceAttnGemm);
+    rc = gemm(st, dS, false, T, dQKV, true, h3, h, (int)h3, T, eq, s, kTraceAttnGemm, false, static_ws);
   } else {
-    rc = gemm(st, X, true, h, dQKV, true, h3, h, (int)h3, T, eq, s, kTraceAttnGemm);
+    rc = gemm(st, X, true, h, dQKV, true, h3, h, (int)h3, T, eq, s, kTraceAttnGemm, false, static_ws);
   }
   if (rc) return rc;
   EpiParams ex{};
@@ -1013,7 +1026,7 @@ static int attn_bwd_impl(const char* what, const QkRopeArgs* rope, const mlp_bf1
   ex.ld = h;
   ex.in0 = residual_grad ? dOut : nullptr;
   ex.out0 = dX;
-  return gemm(st, dQKV, false, h3, Wqkv, false, h3, T, h, (int)h3, ex, s, kTraceAttnGemm);
+  return gemm(st, dQKV, false, h3, Wqkv, false, h3, T, h, (int)h3, ex, s, kTraceAttnGemm, false, static_ws);
 }
 
 int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_t seed, uint64_t token_offset,

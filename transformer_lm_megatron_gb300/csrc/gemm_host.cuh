@@ -95,7 +95,8 @@ int operand_map(CUtensorMap* m, const void* base, bool mn_major, int64_t mn, int
 // static_ws: whether the launch may use the static per-stream workspaces (split tail,
 // tile counters).  The gated block's launches may not: they would tie a result's bits to
 // the stream (only the first few streams have a region) and two graphs captured on one
-// stream, which may run at once on others, to one region.
+// stream, which may run at once on others, to one region.  For the latter reason neither
+// may the launches of attn_rope_fwd and attn_rope_bwd that are captured.
 template <bool AM, bool BM, bool PAIR, bool BATCHED = false, bool WIDE = false, int GATED = kGatedNone>
 int launch_gemm_t(DeviceState* st, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mC,
                   const CUtensorMap& mO0, const CUtensorMap& mO1, int M, int N, int K, const EpiParams& ep,
@@ -480,7 +481,7 @@ int make_map4(CUtensorMap* m, CUtensorMapDataType dt, int esz, const void* base,
 // TMA-only epilogue (kEpiStore: bf16 output; kEpiF32Store / kEpiScaleMask: fp32).
 int gemm_batched(DeviceState* st, const BatchOperand& a, const BatchOperand& b, const BatchOutput& out, int M, int N,
                  int K, int nb_h, int nb_s, const EpiParams& ep, cudaStream_t stream, int trace_kind,
-                 int causal = kCausalNone) {
+                 int causal = kCausalNone, bool static_ws = true) {
   if ((!epi_tma_only(ep.kind) && ep.kind != kEpiSoftmaxGrad) || ep.kind == kEpiF32Add)
     return fail(MLP_EUNSUPPORTED, "batched GEMM: epilogue kind %d not supported", ep.kind);
   const int mode = g_pair_mode.load(std::memory_order_relaxed);
@@ -516,18 +517,18 @@ int gemm_batched(DeviceState* st, const BatchOperand& a, const BatchOperand& b, 
   const int batch = nb_h * nb_s;
   if (!a.mn_major && b.mn_major)
     return pair ? launch_gemm_t<false, true, true, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                         stream, trace_kind, batch, nb_h, causal)
+                                                         stream, trace_kind, batch, nb_h, causal, false, static_ws)
                 : launch_gemm_t<false, true, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                          stream, trace_kind, batch, nb_h, causal);
+                                                          stream, trace_kind, batch, nb_h, causal, false, static_ws);
   if (!a.mn_major && !b.mn_major)
     return pair ? launch_gemm_t<false, false, true, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                          stream, trace_kind, batch, nb_h, causal)
+                                                          stream, trace_kind, batch, nb_h, causal, false, static_ws)
                 : launch_gemm_t<false, false, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                           stream, trace_kind, batch, nb_h, causal);
+                                                           stream, trace_kind, batch, nb_h, causal, false, static_ws);
   if (a.mn_major && b.mn_major)
     return pair ? launch_gemm_t<true, true, true, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                        stream, trace_kind, batch, nb_h, causal)
+                                                        stream, trace_kind, batch, nb_h, causal, false, static_ws)
                 : launch_gemm_t<true, true, false, true>(st, mA, mB, mC, mO0, mO1, M, N, K, ep, raster_n_fast, 0, 0,
-                                                         stream, trace_kind, batch, nb_h, causal);
+                                                         stream, trace_kind, batch, nb_h, causal, false, static_ws);
   return fail(MLP_EUNSUPPORTED, "batched GEMM: operand layout combination not instantiated");
 }
