@@ -9,7 +9,9 @@ constexpr int kFtSmem = 110 * 1024;
 // launch rather than the GEMMs of 256 x 256 tiles: where its tokens fit one tile of 64, and
 // beyond while the weights, read from L2 once for each 64 tokens, stay under a limit: for a
 // pass's first product (G, U and the gate, or dG and dU) of up to 512 tokens 64 MB, for its
-// second (O, or dX) 96 MB.  Measured, few-token / GEMM (us of a pass, the other product alike):
+// second (O, or dX, with `cols` columns) 96 MB where its outputs are those of a tile for a
+// quarter of the SMs or less (with more, the GEMMs fill the SMs).  Measured, few-token / GEMM
+// (us of a pass, the other product alike):
 //   both   48 tokens, h 4096, ffn 16384 66 / 77; h 2048, ffn 5464 21 / 36
 //   first  200 tokens, h 1024, ffn 4096 18 / 21; 192 tokens, h 2048, ffn 5464 34 / 31; 1600
 //          tokens, h 640, ffn 1280 24 / 19; backward: 256 tokens, h 1024, ffn 4096 22 / 25, h
@@ -17,11 +19,17 @@ constexpr int kFtSmem = 110 * 1024;
 //   second 400 tokens, h 1024, ffn 4096 23 / 29; 192 tokens, h 4096, ffn 16384 109 / 92; 1600
 //          tokens, h 1032, ffn 2744 53 / 44; backward: 128 tokens, h 2048, ffn 5464 28 / 37;
 //          512 tokens, h 376, ffn 4752 24 / 34; 1024 tokens, h 1024, ffn 4096 43 / 40
+//          and by the outputs, in tiles of 256 x 256: 8 (1024 tokens, h 512, ffn 1024) 16 / 20;
+//          8 (2048, 256, 2048) 20 / 26; 24 (2048, 768, 1536) 27 / 29; 32 (4096, 512, 1024)
+//          25 / 26; 35 (1500, 1536, 640) 23 / 27; 40 (1024, 2560, 512) 31 / 28; 40 (4096, 640,
+//          1144) 37 / 32; 47 (3000, 1024, 512) 28 / 24; 64 (65536, 64, 256) 59 / 48; backward: 8
+//          (1024, 512, 1024) 20 / 26; 35 (1500, 1536, 640) 26 / 28; 40 (1024, 2560, 512) 33 / 28;
+//          64 (65536, 64, 256) 75 / 58
 bool few_tokens_first(int T, int64_t weight_bytes) {
   return T <= 64 || (T <= 512 && (T + 63) / 64 * weight_bytes <= 64ll << 20);
 }
-bool few_tokens_second(int T, int64_t weight_bytes) {
-  return T <= 64 || (T + 63) / 64 * weight_bytes <= 96ll << 20;
+bool few_tokens_second(const DeviceState* st, int T, int cols, int64_t weight_bytes) {
+  return T <= 64 || ((int64_t)T * cols <= (int64_t)(st->sms / 4) << 16 && (T + 63) / 64 * weight_bytes <= 96ll << 20);
 }
 
 template <int KIND>

@@ -1173,7 +1173,7 @@ int glu_fwd(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed, uint6
   }
   if (rc) return rc;
   const DropoutParams drop = make_dropout(p, seed, token_offset, h);
-  if (few_tokens_second(T, 2ll * h * ffn)) {
+  if (few_tokens_second(st, T, h, 2ll * h * ffn)) {
     f.N = h;
     f.K = ffn;
     f.bias = b;
@@ -1232,7 +1232,7 @@ int glu_bwd_input(int h, int ffn, int t, int64_t tokens, float p, uint64_t seed,
     rc = gemm_dglu(st, g, B, GU, dGU, T, ffn, h, act, s);
   }
   if (rc) return rc;
-  if (few_tokens_second(T, 4ll * h * ffn)) {
+  if (few_tokens_second(st, T, h, 4ll * h * ffn)) {
     f.N = h;
     f.K = 2 * ffn;
     f.in = residual_grad ? dO : nullptr;
