@@ -284,6 +284,8 @@ def qk_norm_rope_fwd(Q, K, Qo, Ko, pos, inv_freq, wq=None, wk=None, eps=1e-6, ro
     """Head norms (with weights wq, wk; none without) and rotation of Q [tokens, nq, d] and K [tokens, nk, d] into
     Qo and Ko.  pos [axes, tokens] int32, inv_freq [rot / 2] fp32, sections: the pairs of each axis."""
     dev = _device()
+    if Q is None or K is None:
+        raise ValueError("Q or K is missing")
     T, nq, d = qs = Q.shape
     nk = K.shape[1]
     ks = (T, nk, d)
@@ -303,6 +305,8 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, dQ, dK, pos, inv_freq, wq=None, wk=None, dw
     """Gradients dQ, dK of qk_norm_rope_fwd from dQo, dKo, and with the norm dwq, dwk [d] fp32 (ws: fp32 workspace of
     qk_norm_rope_workspace(d) floats).  Without the norm Q and K may be None."""
     dev = _device()
+    if dQo is None or dKo is None:
+        raise ValueError("dQo or dKo is missing")
     T, nq, d = qs = dQo.shape
     nk = dKo.shape[1]
     ks = (T, nk, d)
@@ -338,11 +342,17 @@ class Rope:
                           self.interleaved, self.eps, dev)
 
 
+def _p_shape(nh, tokens, seq_len):
+    if seq_len <= 0 or tokens % seq_len:
+        raise ValueError(f"tokens = {tokens} must be a multiple of seq_len = {seq_len} > 0")
+    return tokens // seq_len, nh, seq_len, seq_len
+
+
 def attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, X, Wqkv, bqkv, Wo, bo, R, QKV, QKr, S, P, O,
                   out, stream=None):
     """attn_fwd with the norms and rotation of ``rope`` (a Rope) on its queries and keys; QKr [tokens, 2h] holds them."""
     dev, rows = _device(), (tokens, h)
-    pshape = (tokens // seq_len, nh, seq_len, seq_len)
+    pshape = _p_shape(nh, tokens, seq_len)
     _check(load().attn_rope_fwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens, dev),
                                 _arg("X", X, _bf16, rows, dev), _arg("Wqkv", Wqkv, _bf16, (h, 3 * h), dev),
                                 _arg("bqkv", bqkv, _bf16, (3 * h,), dev), _arg("Wo", Wo, _bf16, (h, h), dev),
@@ -357,7 +367,7 @@ def attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, residu
     """attn_bwd of attn_rope_fwd; rope.dwq and rope.dwk receive the norm weights' gradients.  dP: fp32, at least
     n_seq * nh * seq_len floats."""
     dev, rows = _device(), (tokens, h)
-    pshape = (tokens // seq_len, nh, seq_len, seq_len)
+    pshape = _p_shape(nh, tokens, seq_len)
     if dP is None or dP.dtype is not _float or dP.numel() < tokens * nh or dP.get_device() != dev or not dP.is_contiguous():
         raise ValueError(f"dP must hold at least {tokens * nh} contiguous fp32 on the current device")
     _check(load().attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, *rope.args(tokens, dev),
