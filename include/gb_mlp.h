@@ -46,7 +46,7 @@
  *   - The regions of that memory go by the stream of a call.  A graph keeps the region
  *     of the stream that it was captured on: graphs of mlp_fwd, mlp_bwd, attn_fwd or
  *     attn_bwd captured on one stream must not run at once, nor beside calls on that
- *     stream.  (The other entry points have no such limit.)
+ *     stream.  (mlp_fwd_static_scratch has its own limits; no other entry point has any.)
  *   - Constraints: h > 0, h % 8 == 0; ffn % t == 0, f = ffn/t, f % 8 == 0;
  *     0 < tokens < 2^31; 0 <= p < 1; -1 <= slice < t.
  *   - A kernel that detects a broken pipeline (a bounded wait that ran out)
@@ -223,7 +223,7 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
  *   A [h, 2 ffn] = [Ag | Au], a [2 ffn], GU [tokens, 2 ffn] = [G | U], dGU likewise,
  *   dA [h, 2 ffn], da [2 ffn]; the other shapes, types and constraints as for mlp_fwd
  *   (t must divide ffn, and ffn / t and h be multiples of 8; ffn <= 2^29, h and tokens
- *   <= 2^30).
+ *   <= 2^30).  There are no one-slice calls, so t is checked and changes nothing.
  *
  * glu_fwd: a and b may be NULL (no bias), R NULL means R = X.  GU [tokens, 2 ffn] is
  *   written for the backward and may be NULL; Y [tokens, ffn] is always written.
@@ -231,8 +231,8 @@ int attn_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, uint64_
  * glu_bwd_input: the part of the backward that the block before waits for.  GU as
  *   glu_fwd wrote it.  Writes dGU, dX, and dZ where p > 0; without dropout dZ is dO
  *   and dZ may be NULL.  residual_grad as for mlp_bwd.
- * glu_bwd_weights: the part that only the update waits for, so that a pipeline stage
- *   may send dX on first.  dZ is glu_bwd_input's, or dO where p = 0.  accumulate as
+ * glu_bwd_weights: the part that only the update waits for: a caller may hand dX on
+ *   before it, or run it on another stream.  dZ is glu_bwd_input's, or dO where p = 0.  accumulate as
  *   for mlp_bwd.  da and db may be NULL.  scratch: [tokens, h] fp32, or NULL; holds
  *   the transposed copies of mlp_set_wgrad_transpose where the products are large.
  *
@@ -266,7 +266,7 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
  * Axes: n_axes (1 to 3) rows of positions (e.g. time, height, width).  The first s0
  * pairs turn with axis 0, the next s1 with axis 1, the next s2 with axis 2;
  * s0 + s1 + s2 = rot / 2, and sections of axes that are not there are 0.
- *   tokens in [1, 2^31), nq, nk >= 1 heads of queries and keys; d a multiple of 8, at
+ *   tokens in [1, 2^31), nq, nk in [1, 65536] heads of queries and keys; d a multiple of 8, at
  *   most 256; rot a multiple of 8, 8 <= rot <= d; eps >= 0 (at eps = 0 a head of all
  *   zeros, which then has no norm, gives NaN: its outputs, its gradient, dwq or dwk).
  *   wq, wk [d] bf16 or both NULL; pos [n_axes, tokens] int32 (any value, negative ones
@@ -276,7 +276,8 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
  *   elements apart (a multiple of 8, at least heads * d): the queries and keys inside a
  *   fused projection's output, for instance.  An output may be the same memory as an
  *   input (same pointer and ld); otherwise they may not overlap.
- * Angles are exact to 2^-30 of a turn for any position, where |inv_freq| <= 1.
+ * Angles are off by at most 2^-26 + 2^-31 of a turn (half an fp32 step next to half a
+ * turn) at any position, where |inv_freq| <= 1.
  * Backward: dwq, dwk [d] fp32 are added to (accumulate = 1) or overwritten (0); ws is
  * an fp32 workspace of QK_NORM_ROPE_WS_ROWS * 2 * d floats.  Without the norm (wq and
  * wk NULL) Q, K, dwq, dwk and ws are not used and may be NULL.  Deterministic.
@@ -369,8 +370,8 @@ int mlp_set_cta_pair(int mode);
  * mlp_set_dependent_launch - enable (1, the default) or disable (0), for later
  * calls in this process, programmatic dependent launch: each kernel may be
  * scheduled while the previous kernel on its stream finishes, so its prologue
- * overlaps that kernel's tail; every kernel waits for the previous kernel's
- * results before it touches global memory, so results do not change.
+ * overlaps that kernel's tail; every kernel waits for the previous kernel before it
+ * touches memory that one may write or read, so results do not change.
  * Returns MLP_OK or MLP_EINVAL.
  */
 int mlp_set_dependent_launch(int enable);

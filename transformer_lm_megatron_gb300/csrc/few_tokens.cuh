@@ -18,9 +18,9 @@
 //   kFtDGates  W = B^T: dY, and dG = dY U act'(G), dU = dY act(G)
 //   kFtDX      W = [Ag | Au]^T: dX = [dO +] dGU W
 // The second launch of a pass fetches its first weights before it waits for the first one.
-// One token at h 4096, ffn 16384: 63 us a pass, 94 % of the copy rate (59 us for the
+// One token at h 4096, ffn 16384: 64 us a pass, 93 % of the copy rate (59 us for the
 // weights); 99 us with the GEMMs of 256 x 256 tiles, whose second product has few of them.
-// 27 tokens at h 2048, ffn 5464: 18 us and 35 us (10 us for the weights; a launch takes
+// 27 tokens at h 2048, ffn 5464: 19 us and 35 us (10 us for the weights; a launch takes
 // 2.5 us to its first bytes and 2 us to join and write).
 //
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2..5 TMEM to shared memory; all six

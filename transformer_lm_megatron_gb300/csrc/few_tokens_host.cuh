@@ -1,4 +1,4 @@
-// Host side of the gated block's forward for few tokens: the shape of the launches.
+// Host side of the gated block's products for few tokens: the shape of the launches.
 // Included by gb_mlp.cu inside its anonymous namespace.
 #pragma once
 
@@ -43,7 +43,7 @@ int launch_few_tokens(DeviceState* st, const uint16_t* W, const uint16_t* X, Few
   // CTAs share a tile's reduction until two to an SM are at work, each with 4 k-blocks or
   // more.  A stage is 16 KB of weights and 128 bytes a token; two CTAs share an SM's 227 KB,
   // with three stages each or more beside what they are sent (a CTA by itself leaves its
-  // sums in its own ring).  27 tokens at h 2048, ffn 5464: 18 us; with CTAs for 1.25 or 1.5
+  // sums in its own ring).  27 tokens at h 2048, ffn 5464: 19 us; with CTAs for 1.25 or 1.5
   // to an SM 1 us more, with three small CTAs to an SM (two stages each) 13 us more.
   const int rows = p.T < p.tpad ? p.T : p.tpad, stage_bytes = (int)kFtWBytes + p.tpad * kBK * 2;
   int64_t split = 2 * (int64_t)st->sms / ((int64_t)tiles * token_tiles);

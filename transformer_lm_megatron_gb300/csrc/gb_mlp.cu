@@ -206,8 +206,11 @@ int split_region(DeviceState* st, cudaStream_t stream) {
 
 // Programmatic dependent launch: a kernel may be scheduled while the previous
 // kernel on its stream drains, running its prologue (barriers, TMEM, descriptor
-// prefetch) early; every kernel of this library executes griddepcontrol.wait
-// before its first global-memory access, so results are unchanged.  On by default.
+// prefetch) early; every kernel of this library executes griddepcontrol.wait before
+// its first access to memory that the previous kernel may write or read (the GEMMs look
+// at the status word before it, a late-waiting launch reads and writes what only older
+// kernels touch, the gated block's second few-token launch fetches weights), and before
+// it ends, so results are unchanged.  On by default.
 std::atomic<int> g_pdl{1};
 
 // Launch through cudaLaunchKernelEx with an optional (cx, cy, 1) cluster and the

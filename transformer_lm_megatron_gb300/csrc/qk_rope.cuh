@@ -11,8 +11,9 @@
 // Angles.  A position times a frequency loses all its digits in fp32 once it is
 // some 10^6 radians, so the frequency is taken once per thread in turns as a 64-bit
 // fixed-point fraction; the product with the integer position, modulo 2^64, is then
-// the angle modulo one turn, off by 2^-64 of a turn times the position, and its top 32
-// bits go through sincospi.
+// the angle modulo one turn, off by 2^-64 of a turn times the position.  Its top 32
+// bits go through sincospi as an fp32, whose rounding of up to 2^-26 of a turn is the
+// largest part of the angle's error.
 //
 // Work.  A head is 2 * VEC elements per lane, two vectors of VEC that hold VEC whole
 // pairs, so a lane needs no other lane's elements to turn its own, and a warp holds
@@ -330,7 +331,7 @@ __device__ __forceinline__ void qk_pack_store(uint16_t* dst, const uint64_t (&f)
 // forward (336 MB: 49 us at the copy rate): 123 us with the loads of one step straight into
 // registers, 75 us with four steps in registers; with the ring 57 us at 4 steps, 62 at 6.
 // 8209 x 40 heads of 128 backward (252 MB: 37 us), dw's second launch with it: 47 us at 3
-// or 4 steps, 57 at 2.  What is left is DRAM latency at 16 warps an SM (126 registers; the
+// or 4 steps, 57 at 2.  What is left is DRAM latency at 16 warps an SM (128 registers; the
 // forward at 24 warps is no faster).
 constexpr int kQkDepth = 4;
 
