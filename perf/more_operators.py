@@ -226,7 +226,7 @@ def _write(s):
         codes[block1[grown]] = torch.where(there[:, None, :, None], moved, codes[block1[grown]])
         most[block1] = new
         top = new[run][:, :, None]
-        codes[block[:, None], heads, off[:, None]] = torch.round(x * (127 / top)).to(torch.int8)
+        codes[block[:, None], heads, off[:, None]] = torch.round(x * 127 / top).to(torch.int8)
     return {k: s[k] for k in ("Kc", "Vc", "Kmax", "Vmax")}
 
 
