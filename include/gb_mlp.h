@@ -326,6 +326,68 @@ int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, ui
                   float* dWo, float* dbo, float* dwq, float* dwk, float* ws, void* stream);
 
 /*
+ * The key/value cache in 8 bits, for answering with a model: blocks of bs = 16, 32 or 64 tokens,
+ *   Kc, Vc      [blocks, nk, bs, d] int8   codes, d a multiple of 32, at most 256
+ *   Kmax, Vmax  [blocks, nk] fp32          the largest magnitude of a block's tokens for a head
+ * where a code c stands for c * max / 127.  Request r's token j is at place j % bs of block
+ * table[r][j / bs]; a token's slot is block * bs + place.  A step of a serving loop is
+ *   kv_plan, (the layer's QKV projection), qk_norm_rope_fwd with kv_plan's positions, kv_write, kv_attn
+ * with nothing read back by the host.  Tables, lengths and slots are device memory; what they hold is checked
+ * where it is used, as said below.  Pointers to int32_t and float here need 4-byte alignment only, ws 16.
+ *
+ * kv_plan - where a step's new tokens go.  n <= 4096 requests hold lens[r] tokens and get add[r] new ones
+ * (0 for none).  Blocks that they need beyond those they have, ceil(lens / bs), are taken from the
+ * free list behind its first taken[0] entries, request after request, and entered into the table.
+ *   table      [n, width]  in and out: only the entries of new blocks are written
+ *   lens_out   [n]         lens + add;   taken_out [1]  entries of the free list now taken
+ *   cu         [n + 1]     offsets of the requests' rows: request r has rows cu[r] .. cu[r + 1] - 1
+ *   pos, slots [rows]      each row's position in its request and its slot; rows behind cu[n]
+ *                          (a batch of fixed size) get position 0 and slot -1
+ *   status     [1]         0, or a sum of 1 (not enough free blocks), 2 (a request longer than its
+ *                          table row), 4 (more new tokens than rows), 8 (a negative length):
+ *                          then the step is refused whole: the table stays as it was,
+ *                          lens_out = lens, taken_out = taken, cu = 0, every slot -1.
+ * The outputs must not lie over the inputs (a loop swaps two arrays of lengths).
+ */
+int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* add, const int32_t* lens, int32_t* table,
+            const int32_t* free_list, const int32_t* taken, int32_t* lens_out, int32_t* taken_out, int32_t* cu, int32_t* pos,
+            int32_t* slots, int32_t* status, void* stream);
+
+/*
+ * kv_write - keys and values K, V [tokens, nk, d] (rows ldk, ldv elements apart, multiples of 8) into their
+ * slots; rows with a slot outside [0, blocks * bs) are left out.  For each block and head the
+ * maximum is taken over the new tokens and, where tokens are before them in the block (the first new
+ * one is not at place 0), over what the block held: max = max(max, |x|), code = round(127 x / max), halves
+ * to even, and where the maximum grows the codes before are moved, code = round(code * old / max).  A value is so
+ * off by at most max / 254, and max / 254 more for each time that its block's maximum grew later.  Codes behind the
+ * new tokens are left as they are and mean nothing.
+ *   - The new tokens of one block must be successive rows in successive slots (as kv_plan gives
+ *     them); a call with two such runs in one block, or the same slot twice, has undefined codes there.
+ *   - A block and head with an infinity or a NaN among its tokens reads as NaN; with a
+ *     maximum below 2^-100, as zeros.
+ */
+int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* K, int64_t ldk, const mlp_bf16* V, int64_t ldv,
+             const int32_t* slots, int8_t* Kc, int8_t* Vc, float* Kmax, float* Vmax, void* stream);
+
+/*
+ * kv_attn - attention of each request's rows of Q [rows, nq, d] over its cached tokens, into O (row strides ldq,
+ * ldo, multiples of 8): nq / nk query heads share a key head, softmax(scale Q K^T) V.  lens[r] counts
+ * the new tokens, which are the request's last: its row i of m sees the tokens 0 .. lens[r] - m + i.
+ *   - Rows outside [cu[0], cu[n]) are not touched.  A row that sees no token is written 0.
+ *   - Tokens behind the table row's end (lens > width * bs), and those in a block whose entry is not in
+ *     [0, blocks), are left out.  Offsets cu that fall or leave [0, rows] leave their request out;
+ *     a row that two requests claim holds either's.
+ *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set and are undefined afterwards; calls that may run at once need one each.
+ *   - For few rows a request (single tokens, drafts): every 16 rows times heads read the cache again.
+ * fp32 sums and softmax; queries, codes and softmax weights meet in fp16 (scaled by powers of two, so that
+ * neither range nor more than 2^-12 of a weight is lost).  Results do not depend on what else the GPU runs.
+ */
+#define KV_ATTN_WS_ROWS 19456
+int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int width, float scale, const mlp_bf16* Q, int64_t ldq,
+            const int8_t* Kc, const int8_t* Vc, const float* Kmax, const float* Vmax, const int32_t* table, const int32_t* lens,
+            const int32_t* cu, mlp_bf16* O, int64_t ldo, float* ws, void* stream);
+
+/*
  * mlp_sync_status - synchronise `stream`, then return and clear the device status
  * word: MLP_OK, or MLP_ETIMEOUT if a kernel gave up on a bounded wait since the
  * last call (mlp_last_error() then names the wait), or MLP_ECUDA.
@@ -461,7 +523,8 @@ int mlp_trace_begin(int capacity);
  * X and dZ (mlp_set_wgrad_transpose); 20 = attention GEMMs; 21 =
  * softmax forward / backward; 22 = fused attention core; 30..34 = the gated block's
  * GEMMs G and U with the gate, O, dY with the gate's gradient, dX, dA and dB; 40, 41 =
- * head norms and rotation, forward and backward; 42 = their weight gradients), mnk[3i..3i+2] = the
+ * head norms and rotation, forward and backward; 42 = their weight gradients; 50 = block tables and
+ * slots; 51 = cache write; 52, 53 = attention over the cache, the joining of its parts), mnk[3i..3i+2] = the
  * launch's M, N, K (GEMMs; for the fused core: query rows, keys per sequence, d)
  * or rows, columns, 0, and ms[i] = its device time in milliseconds.  Any output
  * pointer may be NULL.  Returns the number of entries written, or an error code.

@@ -33,6 +33,8 @@
 #include "gb_mlp.h"
 #include "gemm_split.cuh"
 #include "gemm_tc.cuh"
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
 #include "qk_rope.cuh"
 
 using namespace gbmlp;
@@ -76,7 +78,8 @@ enum TraceKind {
   kTraceDropBwd = 10, kTraceColsum = 11, kTraceZero = 12, kTraceOther = 13, kTraceAdam = 14, kTraceTranspose = 15,
   kTraceAttnGemm = 20, kTraceSoftmax = 21, kTraceAttnCore = 22,
   kTraceGlu = 30, kTraceGluOut = 31, kTraceDGlu = 32, kTraceGluDX = 33, kTraceGluDW = 34,
-  kTraceQkRope = 40, kTraceQkRopeBwd = 41, kTraceQkDw = 42
+  kTraceQkRope = 40, kTraceQkRopeBwd = 41, kTraceQkDw = 42,
+  kTraceKvPlan = 50, kTraceKvWrite = 51, kTraceKvAttn = 52, kTraceKvJoin = 53
 };
 
 // Records the start event of the next launch; returns its slot or -1.
@@ -122,6 +125,7 @@ struct DeviceState {
   int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 2) CTAs; last: set up
   bool few_attr[4] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
+  int kv_per_sm[8] = {};    // cache attention, by head size: CTAs to launch on an SM
   int colsum_per_sm[2] = {};  // per column-sum kernel (ColsumKernel): co-resident CTAs on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
@@ -354,6 +358,7 @@ int launch_transposes(cudaStream_t s, int64_t rows, int cols, TransposeJob j0, T
 
 #include "few_tokens_host.cuh"
 #include "qk_rope_host.cuh"
+#include "kv_host.cuh"
 
 template <int CHUNKS>
 cudaError_t softmax_warp_launch(DeviceState* st, const float* S, uint16_t* P, int64_t rows, int cols, cudaStream_t s) {
@@ -1302,6 +1307,103 @@ int glu_bwd_weights(int h, int ffn, int t, int64_t tokens, int accumulate, const
                                       c0, dZ, db, c1, tokens, acc, late);
   trace_post(ts, s, kTraceColsum, tokens, c0 + c1, 0);
   return launch_check(e, "bias-gradient column sums");
+}
+
+// ---------------------------------------------------------------- key/value cache in 8 bits
+int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* add, const int32_t* lens, int32_t* table,
+            const int32_t* free_list, const int32_t* taken, int32_t* lens_out, int32_t* taken_out, int32_t* cu, int32_t* pos,
+            int32_t* slots, int32_t* status, void* stream) {
+  const char* what = "kv_plan";
+  if (bs != 16 && bs != 32 && bs != 64) return fail(MLP_EINVAL, "%s: blocks of %d tokens: 16, 32 or 64 are taken", what, bs);
+  int rc = check_kv_table(what, n, width, bs);
+  if (rc) return rc;
+  if (n_free <= 0) return fail(MLP_EINVAL, "%s: a free list of %d blocks", what, n_free);
+  if (rows <= 0 || rows >= (int64_t)1 << 31) return fail(MLP_EINVAL, "%s: rows = %lld out of range", what, (long long)rows);
+  rc = check_kv_words(what, {{"add", add}, {"lens", lens}, {"table", table}, {"free_list", free_list}, {"taken", taken},
+                             {"lens_out", lens_out}, {"taken_out", taken_out}, {"cu", cu}, {"pos", pos}, {"slots", slots},
+                             {"status", status}});
+  if (rc) return rc;
+  // The CTAs of the launch each read the inputs when they come to them.
+  const std::pair<const void*, int64_t> in[] = {{add, 4ll * n}, {lens, 4ll * n}, {free_list, 4ll * n_free}, {taken, 4}};
+  const std::pair<const void*, int64_t> out[] = {{lens_out, 4ll * n}, {taken_out, 4}, {cu, 4ll * n + 4}, {pos, 4 * rows},
+                                                 {slots, 4 * rows}, {status, 4}, {table, 4ll * n * width}};
+  for (const auto& a : in)
+    for (const auto& b : out)
+      if (overlap(a.first, a.second, b.first, b.second))
+        return fail(MLP_EINVAL, "%s: an output lies over an input (lens_out and taken_out are arrays of their own)", what);
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  KvPlanParams p{n, kv_log2(bs), width, n_free, (int)rows, add, lens, table, free_list, taken, lens_out, taken_out, cu, pos, slots, status};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ts = trace_pre(s);
+  const cudaError_t e = launch_kernel(k_kv_plan, dim3((unsigned)((rows + kKvPlanRows - 1) / kKvPlanRows)), dim3(kKvPlanThreads),
+                                      (2 * (size_t)n + 1) * sizeof(int), s, 1, 1, p);
+  trace_post(ts, s, kTraceKvPlan, rows, n, 0);
+  return launch_check(e, what);
+}
+
+int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* K, int64_t ldk, const mlp_bf16* V, int64_t ldv,
+             const int32_t* slots, int8_t* Kc, int8_t* Vc, float* Kmax, float* Vmax, void* stream) {
+  const char* what = "kv_write";
+  if (tokens <= 0 || tokens >= (int64_t)1 << 31) return fail(MLP_EINVAL, "%s: tokens = %lld out of range", what, (long long)tokens);
+  int rc = check_kv_cache(what, nk, d, bs, blocks);
+  if (!rc) rc = check_qk_rows(what, "K", K, ldk, nk, d);
+  if (!rc) rc = check_qk_rows(what, "V", V, ldv, nk, d);
+  if (!rc) rc = check_ptrs("kv_write (Kc, Vc)", {Kc, Vc});
+  if (!rc) rc = check_kv_words(what, {{"slots", slots}, {"Kmax", Kmax}, {"Vmax", Vmax}});
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  KvWriteParams p{tokens, {ldk, ldv}, nk, blocks, kv_log2(bs), 1, slots, {K, V}, {Kc, Vc}, {Kmax, Vmax}};
+  return launch_kv_write(st, p, d, static_cast<cudaStream_t>(stream));
+}
+
+int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int width, float scale, const mlp_bf16* Q, int64_t ldq,
+            const int8_t* Kc, const int8_t* Vc, const float* Kmax, const float* Vmax, const int32_t* table, const int32_t* lens,
+            const int32_t* cu, mlp_bf16* O, int64_t ldo, float* ws, void* stream) {
+  const char* what = "kv_attn";
+  int rc = check_kv_cache(what, nk, d, bs, blocks);
+  if (!rc) rc = check_kv_table(what, n, width, bs);
+  if (rc) return rc;
+  if (nq <= 0 || nq > 65536 || nq % nk != 0)
+    return fail(MLP_EINVAL, "%s: nq = %d must be a multiple of nk = %d, at most 65536", what, nq, nk);
+  if (rows <= 0 || rows * (nq / nk) >= (int64_t)1 << 31)
+    return fail(MLP_EINVAL, "%s: rows = %lld times %d query heads to a key head must be in [1, 2^31)", what, (long long)rows, nq / nk);
+  if (!(scale > 0.0f && scale <= 3.0e38f)) return fail(MLP_EINVAL, "%s: scale = %g must be positive and finite", what, (double)scale);
+  rc = check_qk_rows(what, "Q", Q, ldq, nq, d);
+  if (!rc) rc = check_qk_rows(what, "O", O, ldo, nq, d);
+  if (!rc && Q == O) rc = fail(MLP_EINVAL, "%s: O must not lie over Q", what);
+  if (!rc) rc = check_ptrs("kv_attn (Kc, Vc, ws)", {Kc, Vc, ws});
+  if (!rc) rc = check_kv_words(what, {{"Kmax", Kmax}, {"Vmax", Vmax}, {"table", table}, {"lens", lens}, {"cu", cu}});
+  if (rc) return rc;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc) return rc;
+  KvAttnParams p{};
+  p.n = n;
+  p.nq = nq;
+  p.nk = nk;
+  p.group = nq / nk;
+  p.width = width;
+  p.log_bs = kv_log2(bs);
+  p.blocks = blocks;
+  p.rows = rows;
+  p.ldq = ldq;
+  p.ldo = ldo;
+  p.scale_log2 = scale * (1.4426950408889634f / 127.0f);
+  p.q = Q;
+  p.kc = Kc;
+  p.vc = Vc;
+  p.kmax = Kmax;
+  p.vmax = Vmax;
+  p.table = table;
+  p.lens = lens;
+  p.cu = cu;
+  p.o = O;
+  p.ws = ws;
+  return launch_kv_attn(st, p, d, static_cast<cudaStream_t>(stream));
 }
 
 int mlp_sync_status(void* stream) {

@@ -1,0 +1,256 @@
+// The key/value cache in 8 bits: which blocks a step's tokens go to, and the write.
+//
+// Blocks of bs = 16, 32 or 64 tokens, a maximum for each block and head:
+//   Kc, Vc [blocks, nk, bs, d] int8, Kmax, Vmax [blocks, nk] fp32;  a code c stands for c * max / 127
+//
+// The maximum is kept, not max / 127: keys and values are bf16, so that products of a code
+// or of 127 with them are exact in fp32 and a division rounded once decides every rounding to
+// a code as exact arithmetic would.  New values are multiplied by 127 / max rounded up instead: of x * 127 /
+// max, quotients of 8-bit significands, a tie is either one where 127 divides max's (then 127 / max is a
+// power of two, the product exact) or +-63.5, at |x| = max / 2, which goes to the even 64 as it does from a
+// little above; everything else is at least 1/510 from a tie, far more than the rounding moves it.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace gbmlp {
+
+constexpr int kKvMaxHead = 256;
+constexpr int kKvMaxRequests = 4096;
+
+// ---------------------------------------------------------------- block tables and slots
+constexpr int kKvPlanThreads = 256;
+constexpr int kKvPlanRows = 1024;  // rows of a CTA
+
+enum KvPlanStatus : int { kKvNoBlocks = 1, kKvTableFull = 2, kKvNoRows = 4, kKvNegative = 8 };
+
+struct KvPlanParams {
+  int n, log_bs, width, n_free, rows;
+  const int* add;
+  const int* lens;
+  int* table;  // [n, width]
+  const int* free;
+  const int* taken;
+  int* lens_out;
+  int* taken_out;
+  int* cu;  // [n + 1]
+  int* pos;
+  int* slots;
+  int* status;
+};
+
+// Inclusive sum over the CTA of a pair; `part` holds a pair for each warp.
+__device__ __forceinline__ void kv_scan2(int64_t& a, int64_t& b, int64_t (*part)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) {
+    const int64_t x = __shfl_up_sync(~0u, a, k), y = __shfl_up_sync(~0u, b, k);
+    if (lane >= k) a += x, b += y;
+  }
+  if (lane == 31) part[warp][0] = a, part[warp][1] = b;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) a += part[w][0], b += part[w][1];
+}
+
+// Every CTA adds up all n requests (a few thousand at most, in L2) and fills in 1024 rows:
+// one launch, nothing handed from CTA to CTA, so what bounds it is that launch and a chain
+// of four loads.
+__global__ void __launch_bounds__(kKvPlanThreads) k_kv_plan(KvPlanParams p) {
+  extern __shared__ int kv_plan_smem[];
+  int* s_cu = kv_plan_smem;           // [n + 1]
+  int* s_first = kv_plan_smem + p.n + 1;  // [n]: new blocks of the requests before
+  __shared__ int64_t part[kKvPlanThreads / 32][2];
+  __shared__ int s_bad;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (threadIdx.x == 0) s_bad = 0;
+  const int bs = 1 << p.log_bs;
+  const int64_t taken = *p.taken;
+  int64_t rows = 0, blocks = 0;
+  int bad = taken < 0 ? kKvNoBlocks : 0;
+  for (int r0 = 0; r0 < p.n; r0 += kKvPlanThreads) {
+    const int r = r0 + (int)threadIdx.x;
+    int64_t add = 0, more = 0;
+    if (r < p.n) {
+      add = p.add[r];
+      int64_t old = p.lens[r];
+      if (add < 0 || old < 0) bad |= kKvNegative, add = add < 0 ? 0 : add, old = old < 0 ? 0 : old;
+      const int64_t need = (old + add + bs - 1) >> p.log_bs;
+      if (need > p.width) bad |= kKvTableFull;
+      more = need - ((old + bs - 1) >> p.log_bs);
+    }
+    int64_t a = add, b = more;
+    __syncthreads();  // `part` and s_bad
+    kv_scan2(a, b, part);
+    if (r < p.n) {
+      s_cu[r] = (int)(rows + a - add);
+      s_first[r] = (int)(blocks + b - more);
+    }
+    for (int w = 0; w < kKvPlanThreads / 32; ++w) rows += part[w][0], blocks += part[w][1];
+  }
+  if (taken + blocks > p.n_free) bad |= kKvNoBlocks;
+  if (rows > p.rows) bad |= kKvNoRows;
+  if (threadIdx.x == 0) s_cu[p.n] = (int)rows;
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  bad = s_bad;
+  if (blockIdx.x == 0) {
+    for (int r = threadIdx.x; r <= p.n; r += kKvPlanThreads) {
+      p.cu[r] = bad ? 0 : s_cu[r];
+      if (r < p.n) p.lens_out[r] = p.lens[r] + (bad ? 0 : p.add[r]);
+    }
+    if (threadIdx.x == 0) {
+      *p.taken_out = (int)(taken + (bad ? 0 : blocks));
+      *p.status = bad;
+    }
+  }
+  const int64_t t_end = min((int64_t)p.rows, ((int64_t)blockIdx.x + 1) * kKvPlanRows);
+  for (int64_t t = (int64_t)blockIdx.x * kKvPlanRows + threadIdx.x; t < t_end; t += kKvPlanThreads) {
+    int pos = 0, slot = -1;
+    if (!bad && t < rows) {
+      int lo = 0, hi = p.n - 1;  // the last request whose rows begin at t or before (the empty ones' end there too)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int old = p.lens[lo];
+      pos = old + (int)(t - s_cu[lo]);
+      const int b = pos >> p.log_bs, have = (int)(((int64_t)old + bs - 1) >> p.log_bs);
+      int* cell = p.table + (int64_t)lo * p.width + b;
+      const int block = b < have ? *cell : p.free[taken + s_first[lo] + b - have];
+      if ((pos & (bs - 1)) == 0) *cell = block;  // a block that begins here is a new one
+      slot = (int)(((unsigned)block << p.log_bs) + (unsigned)(pos & (bs - 1)));
+    }
+    p.pos[t] = pos;
+    p.slots[t] = slot;
+  }
+}
+
+// ---------------------------------------------------------------- the write
+struct KvWriteParams {
+  int64_t tokens, ld[2];  // rows' strides of K, V
+  int nk, blocks, log_bs;
+  int chunk;              // tokens that a CTA looks through for the beginnings of its blocks: at most 32
+  const int* slots;
+  const uint16_t* x[2];
+  int8_t* codes[2];
+  float* most[2];
+};
+
+constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: blocks of smaller magnitudes hold zeros
+constexpr float kKvRound = 12582912.0f;            // 1.5 * 2^23: added, the sum's low byte is the rounded code
+
+// The four codes of fp32 products already rounded into kKvRound's last places.
+__device__ __forceinline__ uint32_t kv_pack4(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+__device__ __forceinline__ uint32_t kv_codes4(uint32_t x01, uint32_t x23, float inv) {
+  return kv_pack4(fmaf(bf16lo(x01), inv, kKvRound), fmaf(bf16hi(x01), inv, kKvRound), fmaf(bf16lo(x23), inv, kKvRound),
+                  fmaf(bf16hi(x23), inv, kKvRound));
+}
+
+__device__ __forceinline__ uint32_t kv_move4(uint32_t codes, float from, float to) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __fdiv_rn((float)(int8_t)(codes >> (8 * i)) * from, to) + kKvRound;
+  return kv_pack4(v[0], v[1], v[2], v[3]);
+}
+
+// One CTA of bs / 16 warps for each `chunk` tokens, head, and keys or values.  Tokens in slots next
+// to each other in one block go together (a run, which begins where the token before is not in the slot
+// before): their rows are read once, into registers (16 tokens of a head to a warp, 16 bytes a
+// lane), their largest magnitude found, their codes written; the codes before them move
+// only where the maximum grows.  Every access is 16 or 8 bytes a lane and side by side, so the
+// copy rate bounds it over many tokens, and a launch with a chain of three loads over few.
+template <int D>
+__global__ void __launch_bounds__(128) k_kv_write(KvWriteParams p) {
+  constexpr int kPieces = D / 16;   // 16-byte pieces of 16 rows that a lane holds
+  constexpr int kRowPieces = D / 8; // of a row
+  __shared__ uint32_t s_most[2][4];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bs = 1 << p.log_bs;
+  int64_t rest = blockIdx.x;
+  const int h = (int)(rest % p.nk);
+  rest /= p.nk;
+  const int kv = (int)(rest & 1);
+  const int64_t t0 = (rest >> 1) * p.chunk;
+  const int64_t cap = (int64_t)p.blocks << p.log_bs;
+  const uint16_t* x = kv ? p.x[1] : p.x[0];
+  const int64_t ld = kv ? p.ld[1] : p.ld[0];
+  uint32_t leads;
+  {
+    const int64_t t = t0 + lane;
+    bool lead = false;
+    if (lane < p.chunk && t < p.tokens) {
+      const int s = p.slots[t], before = t > 0 ? p.slots[t - 1] : -2;
+      lead = s >= 0 && s < cap && ((s & (bs - 1)) == 0 || before != s - 1);
+    }
+    leads = __ballot_sync(~0u, lead);
+  }
+  int turn = 0;
+  while (leads != 0) {
+    const int64_t t = t0 + __ffs(leads) - 1;
+    leads &= leads - 1;
+    const int slot = p.slots[t], off = slot & (bs - 1);
+    int count = 0;  // tokens of the run
+    for (int k = 0; k < bs - off; k += 32) {
+      const int64_t u = t + k + lane;
+      const uint32_t in = __ballot_sync(~0u, k + lane < bs - off && u < p.tokens && p.slots[u] == slot + k + lane);
+      count += in == ~0u ? 32 : __ffs(~in) - 1;
+      if (in != ~0u) break;
+    }
+    const int64_t bh = (int64_t)(slot >> p.log_bs) * p.nk + h;
+    float* most = (kv ? p.most[1] : p.most[0]) + bh;
+    int8_t* codes = (kv ? p.codes[1] : p.codes[0]) + (bh << p.log_bs) * D;
+    const float old = off > 0 ? *most : 0.0f;
+    uint4 v[kPieces];
+    __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int i = lane + 32 * j, at = 16 * warp + i / kRowPieces;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (at >= off && at < off + count)
+        v[j] = *reinterpret_cast<const uint4*>(x + (t + at - off) * ld + (int64_t)h * D + (i % kRowPieces) * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
+        top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
+    // magnitudes in order of their bits, a NaN above all
+    uint32_t bits = (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
+    bits = __reduce_max_sync(~0u, bits);
+    if (bs > 16) {
+      if (lane == 0) s_most[turn][warp] = bits;
+      __syncthreads();
+      for (int w = 0; w < bs / 16; ++w) bits = max(bits, s_most[turn][w]);
+      turn ^= 1;
+    }
+    bits = max(bits, __float_as_uint(old) & 0x7FFFFFFFu);
+    const bool finite = bits < 0x7F800000u;
+    if (!finite) bits = 0x7FC00000u;  // a block with an infinity or a NaN reads as NaN
+    const float now = __uint_as_float(bits);
+    const float inv = finite && now >= kKvTiny ? __fdiv_ru(127.0f, now) : 0.0f;
+    const bool moves = off > 0 && finite && now != old;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int i = lane + 32 * j, at = 16 * warp + i / kRowPieces;
+      uint2* to = reinterpret_cast<uint2*>(codes + at * D + (i % kRowPieces) * 8);
+      if (at >= off && at < off + count) {
+        *to = finite ? make_uint2(kv_codes4(v[j].x, v[j].y, inv), kv_codes4(v[j].z, v[j].w, inv)) : make_uint2(0, 0);
+      } else if (at < off && moves) {
+        const uint2 c = *to;
+        *to = make_uint2(kv_move4(c.x, old, now), kv_move4(c.y, old, now));
+      }
+    }
+    if (threadIdx.x == 0) *most = now;
+  }
+}
+
+}  // namespace gbmlp

@@ -1,0 +1,107 @@
+// Host side of the key/value cache: argument checks and launches.  Included by gb_mlp.cu
+// inside its anonymous namespace.
+#pragma once
+
+static_assert(kKaWsRows == KV_ATTN_WS_ROWS, "the header's workspace");
+
+// Blocks of bs tokens, `blocks` of them, for nk heads of size d.
+int check_kv_cache(const char* what, int nk, int d, int bs, int blocks) {
+  if (nk <= 0 || nk > 65536) return fail(MLP_EINVAL, "%s: nk = %d must be in [1, 65536]", what, nk);
+  if (d <= 0 || d % 32 != 0) return fail(MLP_EINVAL, "%s: head size d = %d must be a positive multiple of 32", what, d);
+  if (d > kKvMaxHead) return fail(MLP_EUNSUPPORTED, "%s: head size d = %d is above %d", what, d, kKvMaxHead);
+  if (bs != 16 && bs != 32 && bs != 64) return fail(MLP_EINVAL, "%s: blocks of %d tokens: 16, 32 or 64 are taken", what, bs);
+  if (blocks <= 0 || (int64_t)blocks * bs >= (int64_t)1 << 31)
+    return fail(MLP_EINVAL, "%s: %d blocks of %d tokens: at least one, and fewer than 2^31 tokens", what, blocks, bs);
+  return MLP_OK;
+}
+
+int kv_log2(int bs) { return bs == 16 ? 4 : bs == 32 ? 5 : 6; }
+
+int check_kv_table(const char* what, int n, int width, int bs) {
+  if (n <= 0 || n > kKvMaxRequests) return fail(MLP_EINVAL, "%s: n = %d requests must be in [1, %d]", what, n, kKvMaxRequests);
+  if (width <= 0 || (int64_t)width * bs >= (int64_t)1 << 31)
+    return fail(MLP_EINVAL, "%s: a table of %d blocks of %d tokens: at least one, and fewer than 2^31 tokens", what, width, bs);
+  return MLP_OK;
+}
+
+// Pointers to 4-byte elements.
+int check_kv_words(const char* what, std::initializer_list<std::pair<const char*, const void*>> ptrs) {
+  for (const auto& p : ptrs) {
+    if (p.second == nullptr) return fail(MLP_EINVAL, "%s: %s is NULL", what, p.first);
+    if ((reinterpret_cast<uintptr_t>(p.second) & 3) != 0) return fail(MLP_EALIGN, "%s: %s is not 4-byte aligned", what, p.first);
+  }
+  return MLP_OK;
+}
+
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+template <int D>
+int launch_kv_write_t(KvWriteParams& p, int64_t ctas, cudaStream_t s) {
+  const int ts = trace_pre(s);
+  const cudaError_t e = launch_kernel(k_kv_write<D>, dim3((unsigned)ctas), dim3(2 << p.log_bs), 0, s, 1, 1, p);
+  trace_post(ts, s, kTraceKvWrite, p.tokens, 2 * (int64_t)p.nk * D, 0);
+  return launch_check(e, "cache write");
+}
+
+int launch_kv_write(const DeviceState* st, KvWriteParams& p, int d, cudaStream_t s) {
+  // A CTA for each token gives a step's single tokens the most CTAs at once; a CTA for each
+  // 16 tokens spares prompts those that find no block beginning at their token.
+  const int64_t each = 2 * (int64_t)p.nk;
+  p.chunk = p.tokens * each <= (int64_t)st->sms * 64 ? 1 : 16;
+  const int64_t ctas = (p.tokens + p.chunk - 1) / p.chunk * each;
+  if (ctas >= (int64_t)1 << 31) return fail(MLP_EUNSUPPORTED, "kv_write: %lld tokens of %d heads are too many for a launch", (long long)p.tokens, p.nk);
+  switch (d / 32) {
+    case 1: return launch_kv_write_t<32>(p, ctas, s);
+    case 2: return launch_kv_write_t<64>(p, ctas, s);
+    case 3: return launch_kv_write_t<96>(p, ctas, s);
+    case 4: return launch_kv_write_t<128>(p, ctas, s);
+    case 5: return launch_kv_write_t<160>(p, ctas, s);
+    case 6: return launch_kv_write_t<192>(p, ctas, s);
+    case 7: return launch_kv_write_t<224>(p, ctas, s);
+    default: return launch_kv_write_t<256>(p, ctas, s);
+  }
+}
+
+template <int D>
+int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
+  auto kern = k_kv_attn<D>;
+  constexpr int smem = KaShape<D>::kBytes;
+  int ctas;
+  {
+    std::lock_guard<std::mutex> lock(g_setup_mu);
+    int& per_sm = st->kv_per_sm[D / 32 - 1];
+    if (per_sm == 0) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      int n = 0;
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kKaThreads, smem);
+      if (e != cudaSuccess || n < 1) return fail(MLP_ECUDA, "cache attention: %s", cudaGetErrorString(e));
+      per_sm = n;
+    }
+    ctas = per_sm * st->sms < kKaMaxCtas ? per_sm * st->sms : kKaMaxCtas;
+  }
+  int ts = trace_pre(s);
+  cudaError_t e = launch_kernel(kern, dim3(ctas), dim3(kKaThreads), smem, s, 1, 1, p);
+  trace_post(ts, s, kTraceKvAttn, p.rows, (int64_t)p.nq * D, 0);
+  const int rc = launch_check(e, "cache attention");
+  if (rc) return rc;
+  ts = trace_pre(s);
+  e = launch_kernel(k_kv_attn_join<D>, dim3(ctas, kKaRows / 4), dim3(128), 0, s, 1, 1, p);
+  trace_post(ts, s, kTraceKvJoin, ctas, D, 0);
+  return launch_check(e, "cache attention, joining");
+}
+
+int launch_kv_attn(DeviceState* st, const KvAttnParams& p, int d, cudaStream_t s) {
+  switch (d / 32) {
+    case 1: return launch_kv_attn_t<32>(st, p, s);
+    case 2: return launch_kv_attn_t<64>(st, p, s);
+    case 3: return launch_kv_attn_t<96>(st, p, s);
+    case 4: return launch_kv_attn_t<128>(st, p, s);
+    case 5: return launch_kv_attn_t<160>(st, p, s);
+    case 6: return launch_kv_attn_t<192>(st, p, s);
+    case 7: return launch_kv_attn_t<224>(st, p, s);
+    default: return launch_kv_attn_t<256>(st, p, s);
+  }
+}

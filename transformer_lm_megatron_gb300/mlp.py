@@ -59,6 +59,9 @@ _SIGNATURES = {
                       + [_vp] * 12 + [_vp]),
     "attn_rope_bwd": (_i32, [_i32, _i32, _i32, _i64, _i32, _f32, _u64, _u64] + [_i32] * 6 + [_f32] + [_vp] * 4
                       + [_i32, _i32] + [_vp] * 21 + [_vp]),
+    "kv_plan": (_i32, [_i32] * 4 + [_i64] + [_vp] * 11 + [_vp]),
+    "kv_write": (_i32, [_i64] + [_i32] * 4 + [_vp, _i64] * 2 + [_vp] * 5 + [_vp]),
+    "kv_attn": (_i32, [_i32, _i64] + [_i32] * 6 + [_f32] + [_vp, _i64] + [_vp] * 7 + [_vp, _i64] + [_vp, _vp]),
     "mlp_trace_begin": (_i32, [_i32]),
     "mlp_trace_end": (_i32, [_i32, _vp, _vp, _vp]),
 }
@@ -173,7 +176,7 @@ def attn_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, residual_grad, ac
 # tensor, and what is wrong is worked out only once something is.
 # ---------------------------------------------------------------------------
 GLU_SILU, GLU_GELU = 0, 1
-_bf16, _float, _int = torch.bfloat16, torch.float32, torch.int32
+_bf16, _float, _int, _int8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -383,6 +386,74 @@ def attn_rope_bwd(h, nh, t, tokens, seq_len, p, seed, token_offset, rope, residu
                                 *_dw_args(rope.d, rope.wq, rope.dwq, rope.dwk, rope.ws, dev), _here(dev, stream)))
 
 
+# ---------------------------------------------------------------------------
+# The key/value cache in 8 bits (include/gb_mlp.h).
+# ---------------------------------------------------------------------------
+class KVCache:
+    """Codes and maxima of a layer's cached keys and values: `blocks` blocks of bs tokens, nk heads of size d."""
+
+    def __init__(self, blocks: int, nk: int, bs: int, d: int, device="cuda"):
+        self.Kc, self.Vc = (torch.zeros(blocks, nk, bs, d, dtype=torch.int8, device=device) for _ in range(2))
+        self.Kmax, self.Vmax = (torch.zeros(blocks, nk, dtype=torch.float32, device=device) for _ in range(2))
+
+
+def _cache(Kc, Vc, Kmax, Vmax, dev):
+    """(blocks, nk, bs, d) of a cache and the pointers of its four tensors."""
+    if Kc is None or Kc.dim() != 4:
+        raise ValueError("Kc must be [blocks, nk, bs, d] int8")
+    blocks, nk, bs, d = shape = Kc.shape
+    return shape, (_arg("Kc", Kc, _int8, shape, dev), _arg("Vc", Vc, _int8, shape, dev), _arg("Kmax", Kmax, _float, (blocks, nk), dev),
+                   _arg("Vmax", Vmax, _float, (blocks, nk), dev))
+
+
+def kv_plan(add, lens, table, free_list, taken, bs, lens_out, taken_out, cu, pos, slots, status, stream=None):
+    """Blocks, rows, positions and slots of a step in which request r gets add[r] tokens to its lens[r].
+    int32: add, lens, lens_out [n], table [n, width] (in and out), free_list, taken, taken_out, status [1], cu [n + 1],
+    pos, slots [rows]."""
+    dev = _device()
+    if add is None or table is None or free_list is None or pos is None or table.dim() != 2:
+        raise ValueError("add, table [n, width], free_list or pos is missing")
+    n, width, rows = add.numel(), table.shape[1], pos.numel()
+    _check(load().kv_plan(n, bs, width, free_list.numel(), rows, _arg("add", add, _int, (n,), dev), _arg("lens", lens, _int, (n,), dev),
+                          _arg("table", table, _int, (n, width), dev),
+                          _arg("free_list", free_list, _int, (free_list.numel(),), dev), _arg("taken", taken, _int, (1,), dev),
+                          _arg("lens_out", lens_out, _int, (n,), dev), _arg("taken_out", taken_out, _int, (1,), dev),
+                          _arg("cu", cu, _int, (n + 1,), dev), _arg("pos", pos, _int, (rows,), dev),
+                          _arg("slots", slots, _int, (rows,), dev), _arg("status", status, _int, (1,), dev), _here(dev, stream)))
+
+
+def kv_write(K, V, slots, Kc, Vc, Kmax, Vmax, stream=None):
+    """K, V [tokens, nk, d] bf16 into their slots [tokens] (int32; none where negative) of the cache."""
+    dev = _device()
+    (blocks, nk, bs, d), cache = _cache(Kc, Vc, Kmax, Vmax, dev)
+    if K is None or K.dim() != 3:
+        raise ValueError("K must be [tokens, nk, d] bf16")
+    shape = (K.shape[0], nk, d)
+    _check(load().kv_write(shape[0], nk, d, bs, blocks, *_rows("K", K, shape, dev), *_rows("V", V, shape, dev),
+                           _arg("slots", slots, _int, shape[:1], dev), *cache, _here(dev, stream)))
+
+
+def kv_attn_workspace(d: int) -> int:
+    """Floats of kv_attn's workspace for heads of size d."""
+    return 19456 * (d + 2)
+
+
+def kv_attn(Q, Kc, Vc, Kmax, Vmax, table, lens, cu, O, ws, scale=None, stream=None):
+    """O = softmax(scale Q K^T) V of each request's rows cu[r] .. cu[r + 1] - 1 over its lens[r] cached tokens, the rows' own
+    the last of them.  Q, O [rows, nq, d] bf16, table [n, width], lens [n], cu [n + 1] int32; scale: 1 / sqrt(d) if None."""
+    dev = _device()
+    (blocks, nk, bs, d), cache = _cache(Kc, Vc, Kmax, Vmax, dev)
+    if Q is None or Q.dim() != 3 or table is None or table.dim() != 2:
+        raise ValueError("Q must be [rows, nq, d] bf16 and table [n, width] int32")
+    rows, nq, _ = Q.shape
+    shape = (rows, nq, d)
+    n, width = table.shape
+    _check(load().kv_attn(n, rows, nq, nk, d, bs, blocks, width, d ** -0.5 if scale is None else scale, *_rows("Q", Q, shape, dev),
+                          *cache, _arg("table", table, _int, (n, width), dev), _arg("lens", lens, _int, (n,), dev),
+                          _arg("cu", cu, _int, (n + 1,), dev), *_rows("O", O, shape, dev),
+                          _arg("ws", ws, _float, (kv_attn_workspace(d),), dev), _here(dev, stream)))
+
+
 class AttnBuffers:
     """Saved activations, workspaces and fp32 gradients of the attention block."""
 
@@ -474,7 +545,8 @@ TRACE_NAMES = {0: "F1 gemm X.A_i +a, GeLU", 1: "F2 gemm Y_i.B_i (+dropout,+resid
                20: "attention GEMM", 21: "softmax, softmax-grad row sums", 22: "fused attention core",
            30: "gated block X.[Ag|Au], gate", 31: "gated block Y.B (+dropout,+residual)",
            32: "gated block dZ.B^T, gate gradient", 33: "gated block dGU.A^T (+dO)", 34: "gated block weight gradients",
-           40: "head norms, rotation", 41: "head norms, rotation backward", 42: "head norm weight gradients"}
+           40: "head norms, rotation", 41: "head norms, rotation backward", 42: "head norm weight gradients",
+           50: "block tables, slots", 51: "cache write", 52: "cache attention", 53: "cache attention, joining"}
 GEMM_KINDS = (0, 1, 2, 3, 4, 5)
 
 
