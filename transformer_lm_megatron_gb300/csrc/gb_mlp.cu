@@ -13,6 +13,7 @@
 //                                  B5  dX (+)= dU_i A_i^T; last slice adds dO and writes bf16
 // The forward sum over slices (operator g of the Megatron MLP) and the backward sum
 // (operator f) are fp32 reductions in HBM on this GPU (STRONGHOLD slides, item 8).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -125,7 +126,7 @@ struct DeviceState {
   int split_clusters[12][kGsMaxSplit] = {};  // per split GEMM: co-resident clusters of 2 (s + 2) CTAs; last: set up
   bool few_attr[4] = {};    // few-token products: dynamic smem attribute set
   int qk_per_sm[16] = {};   // per instantiation of the head norms: CTAs to launch on an SM
-  int kv_per_sm[8] = {};    // cache attention, by head size: CTAs to launch on an SM
+  int kv_per_sm[8][3] = {};  // cache attention, by head size and tile: CTAs to launch on an SM
   int colsum_per_sm[2] = {};  // per column-sum kernel (ColsumKernel): co-resident CTAs on an SM
   int max_pairs[96] = {};   // per CTA-pair instantiation: co-resident clusters of two
 };
@@ -1371,6 +1372,8 @@ int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int 
     return fail(MLP_EINVAL, "%s: nq = %d must be a multiple of nk = %d, at most 65536", what, nq, nk);
   if (rows <= 0 || rows * (nq / nk) >= (int64_t)1 << 31)
     return fail(MLP_EINVAL, "%s: rows = %lld times %d query heads to a key head must be in [1, 2^31)", what, (long long)rows, nq / nk);
+  if ((int64_t)blocks * nk * (bs / 16) >= (int64_t)1 << 31)
+    return fail(MLP_EUNSUPPORTED, "%s: %d blocks of %d heads are too many", what, blocks, nk);
   if (!(scale > 0.0f && scale <= 3.0e38f)) return fail(MLP_EINVAL, "%s: scale = %g must be positive and finite", what, (double)scale);
   rc = check_qk_rows(what, "Q", Q, ldq, nq, d);
   if (!rc) rc = check_qk_rows(what, "O", O, ldo, nq, d);

@@ -6,7 +6,7 @@
 // HBM bounds it: a code is read once and meets 4 * rows operations, rows = new tokens * query heads
 // of a key head.  What counts is that every SM has reads in flight all the time and that a
 // code becomes a matrix operand in few instructions:
-//   - Work is counted in steps of 16 tokens, over all requests, heads and tiles of 16 rows, and cut
+//   - Work is counted in steps of 16 tokens, over all requests, heads and tiles of rows, and cut
 //     into equal shares, one for each CTA that fits on the GPU, wherever that falls: a long request
 //     spreads over all SMs, a ragged batch leaves none idle.  A tile that ends up with several
 //     CTAs leaves its parts (fp32 sums, maximum and denominator of each row) in the workspace, and
@@ -14,11 +14,14 @@
 //   - Each warp takes every fourth step of a share, alone: its lanes copy to shared memory,
 //     asynchronously and some steps ahead, the very bytes that they later feed to the tensor
 //     cores, so there is no barrier in the loop and no transposition: reductions may run
-//     over d and over tokens in any order, so a lane's 16 bytes of a key are the operands of four
-//     successive MMAs, and its 16 bytes of four tokens' values those of 16 column tiles.
+//     over d and over tokens in any order, so a lane's 16 bytes of a key are operands of four
+//     successive MMAs, and its 16 bytes of four tokens' values those of eight.
+//   - Both products are taken transposed, S^T = K Q^T and O^T += V^T P^T: the codes are the operand with 16
+//     rows, the query rows the one with 8, so that eight query rows waste nothing and more of them
+//     (NT times 8) use a converted code again.  P^T changes places within a warp (movmatrix).
 //   - Codes become fp16 exactly (1024 + (c + 128) by a byte permutation, minus 1152): 5 instructions
 //     for 4 keys, 6 for 4 values.  mma.sync, not tcgen05: operands come from registers, where
-//     the codes are converted, and a tile has 16 rows or fewer where tcgen05's has 64 at least.
+//     the codes are converted, and there are as few as 8 rows where tcgen05 wants 128 by 16 out of shared memory.
 //   - Queries go to fp16 with a power of two for each row that brings its largest element below
 //     2^15: exact but for elements under 2^-29 of it.
 //   - A block's value scale goes into the exponent: p' = exp2(s + log2(vscale) - max + 14) is the
@@ -35,12 +38,13 @@ namespace gbmlp {
 
 constexpr int kKaWarps = 4;
 constexpr int kKaThreads = 32 * kKaWarps;
-constexpr int kKaRows = 16;        // query rows of a tile
 constexpr int kKaStep = 16;        // tokens of a step
-constexpr int kKaWsRows = 19456;   // of the workspace, d + 2 floats each: two parts of 16 rows for 608 CTAs
-constexpr int kKaMaxCtas = 600;    // ... of which 8 leave room for the descriptors
+constexpr int kKaWsRows = 19456;   // of the workspace, d + 2 floats each
 constexpr int kKaMinPart = 8;      // steps: no tile is cut nearer than this to either end
+constexpr int kKaTileCost = 8;     // steps that beginning and ending a tile takes as long as
 constexpr float kKaLift = 14.0f;   // p' is at most 2^14
+constexpr int kKaAhead = 4;        // steps of a warp, that many ahead asked for in L2
+constexpr int kKaJoinWarps = 16;
 
 struct KvAttnParams {
   int n, nq, nk, group, width, log_bs, blocks;
@@ -59,24 +63,35 @@ struct KvAttnParams {
   float* ws;
 };
 
-// The workspace: a descriptor of 8 ints for each CTA, then two parts for each (the tile that it begins in
-// the middle of, or its first; and the one that it ends in the middle of): maxima, denominators, sums.
+// The workspace: two descriptors for each CTA, then two parts (maxima, denominators, sums): of the tile that
+// the CTA begins in the middle of, and of the one that it begins and another one goes on with.
 struct KaJoin {
-  int parts, slot, row0, head, tile, rows, pad[2];  // parts: 0 if no tile begins here and goes on elsewhere
+  int first, parts, row0, head, tile, rows, pad[2];  // the CTA that began the tile; 0 parts: there is no such tile
 };
-__host__ __device__ constexpr int64_t ka_part_floats(int d) { return (int64_t)kKaRows * (d + 2); }
-static_assert(kKaMaxCtas * (int64_t)sizeof(KaJoin) + 4 * 2 * kKaMaxCtas * ka_part_floats(32) <= 4 * (int64_t)kKaWsRows * (32 + 2), "the workspace");
+__host__ __device__ constexpr int64_t ka_part_floats(int rows, int d) { return (int64_t)rows * (d + 2); }
+__host__ __device__ constexpr int ka_max_ctas(int rows, int d) {
+  return (int)((int64_t)kKaWsRows * (d + 2) / (2 * (int64_t)(sizeof(KaJoin) / 4) + 2 * ka_part_floats(rows, d)));
+}
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16, 8 or 4 bytes that one lane of the SM reads once.
+__device__ __forceinline__ uint4 ld_once16(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+__device__ __forceinline__ uint2 ld_once8(const int8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint32_t ld_once4(const int8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void prefetch_l2(const int8_t* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -85,11 +100,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // D += A B: 16 x 16 by 16 x 8, fp16, fp32 sums.
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[2]) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+
+// An 8 x 8 matrix of 16-bit elements, two to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Two of four biased codes (c + 128) as fp16: the low pair or the high one.
@@ -106,30 +128,37 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return reinterpret_cast<const uint32_t&>(r);
 }
 
-template <int D>
+// Heads of size D, tiles of 8 NT rows.
+template <int D, int NT>
 struct KaShape {
-  static constexpr int kStages = D <= 128 ? 4 : 3;
-  static constexpr int kCtasPerSm = D <= 160 ? 3 : 2;
-  static constexpr bool kQRegs = D <= 128;              // query operands in registers, else in shared memory
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtasPerSm = NT == 1 ? (D <= 128 ? 4 : D <= 192 ? 3 : 2) : NT == 2 && D <= 128 ? 3 : 2;
+  static constexpr bool kQRegs = NT * D <= 160;         // query operands in registers, else in shared memory
   static constexpr int kK16 = D / 64, kK8 = D / 32 % 2; // key chunks: 16 bytes a lane over 64 d, 8 over 32
   static constexpr int kV16 = D / 128, kV8 = D / 64 % 2, kV4 = D / 32 % 2;  // value chunks: 16, 8, 4 bytes a lane
-  static constexpr int kKBytes = 16 * D, kVBytes = 16 * D;
-  static constexpr int kStage = kKBytes + kVBytes;      // of a warp
-  static constexpr int kRing = kStages * kStage;
   static constexpr int kQPitch = 2 * D + 16;            // bytes of a query row
-  static constexpr int kOPitch = D + 4;                 // floats of a row of a warp's sums, over its ring
-  static_assert(kKaRows * kOPitch * 4 <= kRing, "a warp's sums go over its ring");
-  static constexpr int kOffQ = kKaWarps * kRing;
-  static constexpr int kOffScale = kOffQ + kKaRows * kQPitch;          // float4 for each warp and stage
-  static constexpr int kOffRow = kOffScale + kKaWarps * kStages * 16;  // fp32 for each row: query scale
-  static constexpr int kOffMax = kOffRow + kKaRows * 4;                // [warps][rows] maxima, denominators
-  static constexpr int kBytes = kOffMax + 2 * kKaWarps * kKaRows * 4;
+  static constexpr int kOPitch = D + 4;                 // floats of a row of sums
+  static constexpr int kOffPlace = 0;                                 // KaPlace of 64 steps of each warp
+  static constexpr int kOffQ = kOffPlace + kKaWarps * 64 * 16;
+  static constexpr int kOffO = kOffQ + kRows * kQPitch;
+  static constexpr int kOffRow = kOffO + kRows * kOPitch * 4;         // query scale of each row, then 1 / denominator
+  static constexpr int kOffMax = kOffRow + 2 * kRows * 4;             // [warps][rows] maxima, denominators
+  static constexpr int kBytes = kOffMax + 2 * kKaWarps * kRows * 4;
 };
 
-// A request as the work is counted: its rows and steps.
+// Where a step's tokens are, in units of 16 tokens of a head from the pools' beginnings (complemented if their
+// block is not there: what it says is read all the same, and masked), and their scales.
+struct __align__(16) KaPlace {
+  int unit;
+  float kscale, vlog, vinv;
+};
+
+// A request as the work is counted: its rows, and its steps.
 struct KaRequest {
   int row0, fresh, len, held, tiles, steps;  // held: the tokens that its table row has room for
+  __device__ __forceinline__ int64_t weight(int nk) const { return (int64_t)tiles * nk * (steps + kKaTileCost); }
 };
+template <int ROWS>
 __device__ __forceinline__ KaRequest ka_request(const KvAttnParams& p, int r) {
   KaRequest q;
   const int a = p.cu[r], b = p.cu[r + 1], len = p.lens[r];
@@ -138,21 +167,27 @@ __device__ __forceinline__ KaRequest ka_request(const KvAttnParams& p, int r) {
   q.fresh = a >= 0 && b > a && b <= p.rows ? b - a : 0;
   q.len = max(0, len);
   q.held = (int)min((int64_t)q.len, most);
-  q.tiles = (int)(((int64_t)q.fresh * p.group + kKaRows - 1) / kKaRows);
+  q.tiles = (int)(((int64_t)q.fresh * p.group + ROWS - 1) / ROWS);
   q.steps = max(1, (int)(((int64_t)q.held + kKaStep - 1) / kKaStep));
   return q;
 }
 
-// Its steps over all heads and tiles (0 behind the last request).
-__device__ __forceinline__ int64_t ka_weight(const KvAttnParams& p, int r) {
-  if (r >= p.n) return 0;
-  const KaRequest q = ka_request(p, r);
-  return (int64_t)q.tiles * q.steps * p.nk;
+// The steps [step0, step1) of a tile that a CTA takes.
+struct KaItem {
+  KaRequest rq;
+  int r, h, tile, step0, step1, my_steps;
+  int64_t end;  // of the tile in the work
+};
+
+// a / b and its rest, a >= 0, b > 0: in 32 bits where they fit.
+__device__ __forceinline__ int64_t ka_div(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kKaThreads, KaShape<D>::kCtasPerSm) k_kv_attn(KvAttnParams p) {
-  using S = KaShape<D>;
+template <int D, int NT>
+__global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_attn(KvAttnParams p) {
+  using S = KaShape<D, NT>;
+  constexpr int ROWS = S::kRows;
   extern __shared__ __align__(16) uint8_t ka_smem[];
   __shared__ int64_t s_part[kKaWarps];
   __shared__ int64_t s_cut[2], s_begin;
@@ -163,438 +198,505 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D>::kCtasPerSm) k_kv_attn(
   grid_launch_dependents();
 
   // ------------------------------------------------------------ the share
-  int64_t total = 0;
-  for (int r = tid; r < p.n; r += kKaThreads) total += ka_weight(p, r);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(~0u, total, k);
-  if (lane == 0) s_part[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < kKaWarps; ++w) total += s_part[w];
-  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kKaMinPart);
-  const int64_t raw[2] = {min(total, share * blockIdx.x), min(total, share * (blockIdx.x + 1))};
-  if (tid == 0) s_cut[0] = raw[0], s_cut[1] = raw[1], s_first = p.n, s_begin = total;
-  int64_t carry = 0;
-  for (int r0 = 0; r0 < p.n && carry <= raw[1]; r0 += kKaThreads) {
-    const int64_t w = ka_weight(p, r0 + tid);
-    int64_t inc = w;
+  // (the requests in groups of 128: the first group's sums are kept, a further one's are worked out again)
+  int64_t weight = 0, inc = 0, total = 0;
+  int steps = 1;
+  auto group_sums = [&](int r0) {  // weight, its inclusive sum, and the group's total
+    weight = 0;
+    if (r0 + tid < p.n) {
+      const KaRequest q = ka_request<ROWS>(p, r0 + tid);
+      weight = q.weight(p.nk);
+      steps = q.steps;
+    }
+    inc = weight;
 #pragma unroll
     for (int k = 1; k < 32; k *= 2) {
       const int64_t x = __shfl_up_sync(~0u, inc, k);
       if (lane >= k) inc += x;
     }
-    __syncthreads();  // s_part, s_cut
     if (lane == 31) s_part[warp] = inc;
     __syncthreads();
-    int64_t all = 0, before = carry;
+    int64_t all = 0;
     for (int k = 0; k < kKaWarps; ++k) {
-      if (k < warp) before += s_part[k];
+      if (k < warp) inc += s_part[k];
       all += s_part[k];
     }
-    const int64_t begin = before + inc - w;
-    if (w > 0) {
-      const int steps = ka_request(p, r0 + tid).steps;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (raw[k] >= begin && raw[k] < begin + w) {
-          const int64_t in = (raw[k] - begin) % steps;  // a cut near an end of a tile goes there
-          const int64_t cut = in < kKaMinPart ? raw[k] - in : steps - in < kKaMinPart ? raw[k] - in + steps : raw[k];
-          s_cut[k] = cut;
-          if (k == 0) s_first = r0 + tid, s_begin = begin;
-        }
-    }
-    carry += all;
+    return all;
+  };
+  for (int r0 = (p.n - 1) / kKaThreads * kKaThreads; r0 >= 0; r0 -= kKaThreads) {
+    total += group_sums(r0);
+    if (r0 > 0) __syncthreads();
   }
+  const int64_t share = max(ka_div(total + gridDim.x - 1, gridDim.x), (int64_t)kKaMinPart);
+  const int64_t raw[2] = {min(total, share * blockIdx.x), min(total, share * (blockIdx.x + 1))};
+  if (tid == 0) s_cut[0] = raw[0], s_cut[1] = raw[1], s_first = p.n, s_begin = total;
   __syncthreads();
+  int64_t carry = 0;
+  for (int r0 = 0;;) {
+    const int64_t begin = carry + inc - weight;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (raw[k] >= begin && raw[k] < begin + weight) {
+        // a tile's cost comes before its steps; a cut near an end of a tile goes there
+        const int64_t ahead = raw[k] - begin;
+        const int in = (int)(ahead - ka_div(ahead, steps + kKaTileCost) * (steps + kKaTileCost)), step = in - kKaTileCost;
+        s_cut[k] = raw[k] + (step < kKaMinPart ? -in : steps - step < kKaMinPart ? steps - step : 0);
+        if (k == 0) s_first = r0 + tid, s_begin = begin;
+      }
+    for (int k = 0; k < kKaWarps; ++k) carry += s_part[k];
+    __syncthreads();
+    r0 += kKaThreads;
+    if (r0 >= p.n || carry > raw[1]) break;
+    group_sums(r0);
+  }
   int64_t at = s_cut[0];
   const int64_t end = s_cut[1];
-  int r = s_first;
+  KaJoin* joins = reinterpret_cast<KaJoin*>(p.ws) + 2 * blockIdx.x;
+  if (tid < 2) joins[tid].parts = 0;
+  if (at >= end) return;
+  float* parts = p.ws + 2 * (int64_t)gridDim.x * (sizeof(KaJoin) / 4);
   int64_t begin = s_begin;
-  KaJoin join = {};
-  float* parts = p.ws + (int64_t)kKaMaxCtas * (sizeof(KaJoin) / 4);
-  bool first = true;
 
-  uint8_t* ring = ka_smem + warp * S::kRing;
-  const uint32_t ring_u = smem_u32(ring);
-  float4* scales = reinterpret_cast<float4*>(ka_smem + S::kOffScale) + warp * S::kStages;
+  KaPlace* places = reinterpret_cast<KaPlace*>(ka_smem + S::kOffPlace) + warp * 64;
   float* s_qscale = reinterpret_cast<float*>(ka_smem + S::kOffRow);
+  float* s_inv = s_qscale + ROWS;
   float* s_max = reinterpret_cast<float*>(ka_smem + S::kOffMax);
-  float* s_den = s_max + kKaWarps * kKaRows;
+  float* s_den = s_max + kKaWarps * ROWS;
+  float* s_o = reinterpret_cast<float*>(ka_smem + S::kOffO);
 
-  while (at < end) {
-    // ---------------------------------------------------------- the next tile's steps [step0, step1)
-    KaRequest rq = ka_request(p, r);
-    while (at >= begin + (int64_t)rq.tiles * rq.steps * p.nk) {  // (ends: at < total, the last request's end)
-      begin += (int64_t)rq.tiles * rq.steps * p.nk;
-      rq = ka_request(p, ++r);
+  // The tile that `at` is in (at < end, so there is one).
+  KaItem it;
+  it.r = s_first;
+  it.rq = ka_request<ROWS>(p, it.r);
+  auto next_item = [&]() {
+    while (at >= begin + it.rq.weight(p.nk)) {
+      begin += it.rq.weight(p.nk);
+      it.rq = ka_request<ROWS>(p, ++it.r);
     }
-    const int64_t item = (at - begin) / rq.steps;
-    const int step0 = (int)(at - begin - item * rq.steps);
-    const int step1 = (int)min((int64_t)rq.steps, step0 + (end - at));
-    const int h = (int)(item / rq.tiles), tile = (int)(item - (int64_t)h * rq.tiles);
-    const int tile_rows = (int)min((int64_t)kKaRows, (int64_t)rq.fresh * p.group - (int64_t)tile * kKaRows);
-    const int64_t item_end = at - step0 + rq.steps;
-    const int* table = p.table + (int64_t)r * p.width;
-    const int my_steps = max(0, (step1 - step0 - warp + kKaWarps - 1) / kKaWarps);
-    // the tokens that a row sees: those before its place behind the older ones
-    auto sees = [&](int row) { return min(rq.held, rq.len - rq.fresh + (tile * kKaRows + row) / p.group + 1); };
-    const int seen_by_all = sees(0);
+    const int whole = it.rq.steps + kKaTileCost;
+    const int64_t item = ka_div(at - begin, whole);
+    it.end = begin + (item + 1) * whole;
+    it.h = (int)ka_div(item, it.rq.tiles);
+    it.tile = (int)(item - (int64_t)it.h * it.rq.tiles);
+    it.step0 = max(0, (int)(at - (it.end - it.rq.steps)));
+    it.step1 = it.rq.steps - (int)max((int64_t)0, it.end - end);
+    it.my_steps = max(0, (it.step1 - it.step0 - warp + kKaWarps - 1) / kKaWarps);
+  };
 
-    // ---------------------------------------------------------- copies
-    // lane l looks up the blocks and scales of the warp's steps l, l + 32, ...
-    int blk = -1;
-    float4 sc;
-    auto look_up = [&](int i0) {
-      const int i = i0 + lane;
-      blk = -1;
-      sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i < my_steps) {
-        const int token = (step0 + warp + kKaWarps * i) * kKaStep;
-        const int b = token < rq.held ? table[token >> p.log_bs] : -1;
-        if (b >= 0 && b < p.blocks) {
-          blk = b;
-          const int64_t bh = (int64_t)b * p.nk + h;
-          const float v = fmaxf(p.vmax[bh] * (1.0f / 127.0f), 7.703719777548943e-34f);  // 2^-110 (keeps no NaN)
-          const bool nan = !(p.vmax[bh] <= 3.4028234663852886e38f);
-          sc.x = p.kmax[bh];
-          sc.y = nan ? __uint_as_float(0x7FC00000u) : log2f(v);
-          sc.z = nan ? 0.0f : __fdividef(1.0f, v);
-          sc.w = 1.0f;
+  // ------------------------------------------------------------ reads
+  // lane l looks up the places of the warp's steps i0 + l; where those are a tile's first, it asks for the first
+  // few's codes as soon as it knows where they are
+  auto look_up = [&](int i0) {
+    const int i = i0 + lane;
+    KaPlace pl = {~0, 0.0f, 0.0f, 0.0f};
+    if (i < it.my_steps) {
+      const int token = (it.step0 + warp + kKaWarps * i) * kKaStep;
+      const int b = token < it.rq.held ? p.table[(int64_t)it.r * p.width + (token >> p.log_bs)] : -1;
+      if (b >= 0 && b < p.blocks) {
+        const int64_t bh = (int64_t)b * p.nk + it.h;
+        pl.unit = (int)(bh << (p.log_bs - 4)) + ((token & ((1 << p.log_bs) - 1)) >> 4);
+        const float most = p.vmax[bh], kmost = p.kmax[bh];
+        if (i < kKaAhead) {
+          prefetch_l2(p.kc + (int64_t)pl.unit * (16 * D), 16 * D);
+          prefetch_l2(p.vc + (int64_t)pl.unit * (16 * D), 16 * D);
         }
+        const float v = fmaxf(most * (1.0f / 127.0f), 7.703719777548943e-34f);  // at least 2^-110
+        const bool fine = most <= 3.4028234663852886e38f;
+        pl.kscale = kmost;
+        pl.vlog = fine ? log2f(v) : __uint_as_float(0x7FC00000u);
+        pl.vinv = fine ? __fdividef(1.0f, v) : 0.0f;
       }
-    };
-    auto issue = [&](int i) {
-      if (i < my_steps) {
-        if ((i & 31) == 0) look_up(i);
-        const int stage = i % S::kStages;
-        const int b = __shfl_sync(~0u, blk, i & 31);
-        if (lane == (i & 31)) scales[stage] = sc;
-        if (b >= 0) {
-          const int token = (step0 + warp + kKaWarps * i) * kKaStep;
-          const int64_t base = ((((int64_t)b * p.nk + h) << p.log_bs) + (token & ((1 << p.log_bs) - 1))) * D;
-          const uint32_t dst = ring_u + stage * S::kStage;
-          const int8_t* k = p.kc + base + g * D;
+    }
+    __syncwarp();  // the places that these take the slots of have been read
+    places[i & 63] = pl;
+    __syncwarp();
+  };
+  auto offset = [&](int unit) { return (int64_t)max(unit, ~unit) * (16 * D); };
+  // asks for step i's codes in L2
+  auto ahead = [&](int i) {
+    if (i >= it.my_steps) return;
+    if ((i & 31) == 0) look_up(i);
+    if (lane < 2) prefetch_l2((lane == 0 ? p.kc : p.vc) + offset(places[i & 63].unit), 16 * D);
+  };
+  uint4 k16[S::kK16 ? S::kK16 : 1][2], v16[S::kV16 ? S::kV16 : 1][4];
+  uint2 k8[2], v8[4];
+  uint32_t v4[4];
+  auto load_keys = [&](int64_t off) {
+    const int8_t* k = p.kc + off + g * D + 16 * t;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int c = 0; c < S::kK16; ++c)
-              cp_async16(dst + ((j * S::kK16 + c) * 32 + lane) * 16, k + j * 8 * D + 64 * c + 16 * t);
-            if constexpr (S::kK8 != 0)
-              cp_async_small<8>(dst + 2 * S::kK16 * 512 + (j * 32 + lane) * 8, k + j * 8 * D + 64 * S::kK16 + 8 * t);
-          }
-          const int8_t* v = p.vc + base + 2 * t * D;
-          const uint32_t vd = dst + S::kKBytes;
+      for (int c = 0; c < S::kK16; ++c) k16[c][j] = ld_once16(k + j * 8 * D + 64 * c);
+      if constexpr (S::kK8 != 0) k8[j] = ld_once8(k + j * 8 * D + 64 * S::kK16 - 8 * t);
+    }
+  };
+  auto load_values = [&](int64_t off) {
+    const int8_t* v = p.vc + off + 2 * t * D;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int8_t* vr = v + ((u & 1) + 8 * (u >> 1)) * D;
+    for (int u = 0; u < 4; ++u) {
+      const int8_t* row = v + ((u & 1) + 8 * (u >> 1)) * D;
 #pragma unroll
-            for (int c = 0; c < S::kV16; ++c) cp_async16(vd + ((u * S::kV16 + c) * 32 + lane) * 16, vr + 128 * c + 16 * g);
-            if constexpr (S::kV8 != 0)
-              cp_async_small<8>(vd + 4 * S::kV16 * 512 + (u * 32 + lane) * 8, vr + 128 * S::kV16 + 8 * g);
-            if constexpr (S::kV4 != 0)
-              cp_async_small<4>(vd + 4 * S::kV16 * 512 + 4 * S::kV8 * 256 + (u * 32 + lane) * 4,
-                                vr + 128 * S::kV16 + 64 * S::kV8 + 4 * g);
-          }
-        }
-      }
-      cp_async_commit();
-    };
+      for (int c = 0; c < S::kV16; ++c) v16[c][u] = ld_once16(row + 128 * c + 16 * g);
+      if constexpr (S::kV8 != 0) v8[u] = ld_once8(row + 128 * S::kV16 + 8 * g);
+      if constexpr (S::kV4 != 0) v4[u] = ld_once4(row + 128 * S::kV16 + 64 * S::kV8 + 4 * g);
+    }
+  };
+  // 16 lanes to a query row, 8 rows at a time (those behind the tile's last: zeros)
+  uint32_t qx[NT][D / 32];
+  auto tile_rows_of = [&](const KaItem& x) { return (int)min((int64_t)ROWS, (int64_t)x.rq.fresh * p.group - (int64_t)x.tile * ROWS); };
+  auto load_queries = [&]() {
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int q = 0; q < NT; ++q) {
+      const int row = 8 * q + (tid >> 4), idx = it.tile * ROWS + row, i = idx / p.group;
+      const bool there = row < tile_rows_of(it);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (it.rq.row0 + i) * p.ldq + ((int64_t)it.h * p.group + (idx - i * p.group)) * D);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) qx[q][j] = there ? __ldg(src + 16 * j + (tid & 15)) : 0u;
+    }
+  };
+  KaPlace place;
+  int64_t off = 0;
+  auto begin_item = [&]() {
+    next_item();
+    load_queries();
+    if (it.my_steps == 0) return;
+    look_up(0);
+    place = places[0];
+    off = offset(place.unit);
+    load_keys(off);
+    load_values(off);
+  };
+  begin_item();
+
+  while (true) {
+    const int tile_rows = tile_rows_of(it);
+    // the tokens that a row sees: those before its place behind the older ones
+    auto sees = [&](int row) { return min(it.rq.held, it.rq.len - it.rq.fresh + (it.tile * ROWS + row) / p.group + 1); };
+    // the warp's steps from here on have tokens that some row does not see
+    const int from = sees(0) / kKaStep - it.step0 - warp, first_masked = from <= 0 ? 0 : (from + kKaWarps - 1) / kKaWarps;
 
     // ---------------------------------------------------------- queries
-    // 8 lanes to a row: its largest exponent, then fp16 (rows behind the tile's last: zeros)
-    {
-      const int row = tid >> 3, part = tid & 7;
-      constexpr int kEach = D / 8;  // elements of a lane, in pairs
-      uint32_t x[kEach / 2];
-      const bool there = row < tile_rows;
-      const int64_t idx = (int64_t)tile * kKaRows + row;
-      const uint32_t* src = nullptr;
-      if (there) {
-        const int64_t i = idx / p.group;
-        src = reinterpret_cast<const uint32_t*>(p.q + (rq.row0 + i) * p.ldq + ((int64_t)h * p.group + (idx - i * p.group)) * D) +
-              part * (kEach / 2);
-      }
+    // to fp16, by the largest element's exponent
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      const int row = 8 * q + (tid >> 4), part = tid & 15;
       uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < kEach / 2; ++j) {
-        x[j] = there ? src[j] : 0u;
-        top = max(top, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-      }
+      for (int j = 0; j < D / 32; ++j) top = max(top, max(qx[q][j] & 0x7FFFu, (qx[q][j] >> 16) & 0x7FFFu));
 #pragma unroll
-      for (int k = 1; k < 8; k *= 2) top = max(top, __shfl_xor_sync(~0u, top, k));
-      // the exponent of 2^(14 - e), e that of the largest element (kept where both powers are normal numbers)
+      for (int k = 1; k < 16; k *= 2) top = max(top, __shfl_xor_sync(~0u, top, k));
+      // 2^(14 - e), e the exponent of the largest element (kept where both powers are normal numbers)
       const int e = min(max((int)(top >> 7) - 127, -100), 127);
       const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(ka_smem + S::kOffQ + row * S::kQPitch) + part * (kEach / 2);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(ka_smem + S::kOffQ + row * S::kQPitch);
 #pragma unroll
-      for (int j = 0; j < kEach / 2; ++j) dst[j] = pack_half2(bf16lo(x[j]) * up, bf16hi(x[j]) * up);
+      for (int j = 0; j < D / 32; ++j) dst[16 * j + part] = pack_half2(bf16lo(qx[q][j]) * up, bf16hi(qx[q][j]) * up);
       if (part == 0) s_qscale[row] = p.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
     }
     __syncthreads();
-    // the operands of k-step s of a 64-wide chunk c: words 2 s and 2 s + 1 of a lane's 16 elements, rows g and g + 8
+    // the operands of k-steps s and s + 1 of a 64-wide chunk c (or the 32-wide one): elements 4 s .. 4 s + 7 of row g
     const uint8_t* qrow = ka_smem + S::kOffQ + g * S::kQPitch;
-    constexpr int kChunks = S::kK16 + S::kK8;
-    uint32_t qa[S::kQRegs ? D / 16 : 1][4];
-    auto load_q = [&](int chunk, int s, uint32_t (&a)[4]) {  // a wide chunk's lane holds 16 elements, the narrow one's 8
-      const int off = chunk < S::kK16 ? chunk * 128 + 32 * t + 8 * s : S::kK16 * 128 + 16 * t + 8 * s;
-      const uint2 x = *reinterpret_cast<const uint2*>(qrow + off), y = *reinterpret_cast<const uint2*>(qrow + 8 * S::kQPitch + off);
-      a[0] = x.x, a[1] = y.x, a[2] = x.y, a[3] = y.y;
+    auto load_q = [&](int chunk, int s, int nt, uint32_t (&x)[2], uint32_t (&y)[2]) {
+      const int at_byte = chunk < S::kK16 ? chunk * 128 + 32 * t + 8 * s : S::kK16 * 128 + 16 * t + 8 * s;
+      const uint4 v = *reinterpret_cast<const uint4*>(qrow + nt * 8 * S::kQPitch + at_byte);
+      x[0] = v.x, x[1] = v.y, y[0] = v.z, y[1] = v.w;
     };
+    uint32_t qb[S::kQRegs ? D / 16 : 2][NT][2];
     if constexpr (S::kQRegs) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+      for (int c = 0; c < S::kK16 + S::kK8; ++c)
 #pragma unroll
-        for (int s = 0; s < (c < S::kK16 ? 4 : 2); ++s) load_q(c, s, qa[4 * c + s]);
+        for (int s = 0; s < (c < S::kK16 ? 4 : 2); s += 2)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) load_q(c, s, nt, qb[4 * c + s][nt], qb[4 * c + s + 1][nt]);
     }
-    const float qs0 = s_qscale[g], qs1 = s_qscale[g + 8];
-    const int see0 = g < tile_rows ? sees(g) : 0x7FFFFFFF, see1 = g + 8 < tile_rows ? sees(g + 8) : 0x7FFFFFFF;
+    float qs[NT][2];
+    int see[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * nt + 2 * t + e;
+        qs[nt][e] = s_qscale[row];
+        see[nt][e] = row < tile_rows ? sees(row) : 0x7FFFFFFF;
+      }
 
     // ---------------------------------------------------------- the steps
-    float o[D / 8][4];
+    float o[D / 16][NT][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    float m0 = -INFINITY, m1 = -INFINITY, b0 = -kKaLift, b1 = -kKaLift, l0 = 0.0f, l1 = 0.0f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    float m[NT][2], b[NT][2], l[NT][2];  // maximum, what is taken off a score, denominator
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, b[nt][e] = -kKaLift, l[nt][e] = 0.0f;
 
-    for (int i = 0; i < my_steps; ++i) {
-      cp_async_wait<S::kStages - 2>();
-      __syncwarp();
-      const int stage = i % S::kStages;
-      const uint8_t* sk = ring + stage * S::kStage;
-      const float4 scale = scales[stage];
-      float c[2][4];
+    for (int i = 0; i < it.my_steps; ++i) {
+      const KaPlace scale = place;
+      ahead(i + kKaAhead);
+      if (i + 1 < it.my_steps) {
+        place = places[(i + 1) & 63];
+        off = offset(place.unit);
+      }
+      float c[NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
+      // two k-steps: a word each of the keys of tokens g and g + 8
+      auto keys = [&](int chunk, int s, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        if constexpr (!S::kQRegs) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) load_q(chunk, s, nt, qb[0][nt], qb[1][nt]);
+        }
+        const int at_q = S::kQRegs ? 4 * chunk + s : 0;
+        const uint32_t x = w0 ^ 0x80808080u, y = w1 ^ 0x80808080u, z = w2 ^ 0x80808080u, w = w3 ^ 0x80808080u;
+        const uint32_t x0 = codes_lo(x), x1 = codes_hi(x), y0 = codes_lo(y), y1 = codes_hi(y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], x0, y0, x1, y1, qb[at_q][nt]);
+        const uint32_t z0 = codes_lo(z), z1 = codes_hi(z), w0h = codes_lo(w), w1h = codes_hi(w);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], z0, w0h, z1, w1h, qb[at_q + 1][nt]);
+      };
 #pragma unroll
       for (int ch = 0; ch < S::kK16; ++ch) {
+        keys(ch, 0, k16[ch][0].x, k16[ch][1].x, k16[ch][0].y, k16[ch][1].y);
+        keys(ch, 2, k16[ch][0].z, k16[ch][1].z, k16[ch][0].w, k16[ch][1].w);
+      }
+      if constexpr (S::kK8 != 0) keys(S::kK16, 0, k8[0].x, k8[1].x, k8[0].y, k8[1].y);
+      if (i + 1 < it.my_steps) load_keys(off);
+      // scores in powers of two, the block's value scale among them: token g + 8 (j / 2), row 2 t + j % 2
+      bool grows = false;
+      const int token = (it.step0 + warp + kKaWarps * i) * kKaStep;
+      const bool masked = i >= first_masked || scale.unit < 0;  // (there is no such block)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sk + ((j * S::kK16 + ch) * 32 + lane) * 16);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t x = ws[s] ^ 0x80808080u;
-            if constexpr (S::kQRegs) {
-              mma_f16(c[j], qa[4 * ch + s], codes_lo(x), codes_hi(x));
-            } else {
-              uint32_t a[4];
-              load_q(ch, s, a);
-              mma_f16(c[j], a, codes_lo(x), codes_hi(x));
-            }
-          }
+        for (int j = 0; j < 4; ++j) c[nt][j] = fmaf(c[nt][j], qs[nt][j & 1] * scale.kscale, scale.vlog);
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (token + g + 8 * (j >> 1) >= see[nt][j & 1] || scale.unit < 0) c[nt][j] = -INFINITY;
         }
+        grows |= fmaxf(c[nt][0], c[nt][2]) > m[nt][0] || fmaxf(c[nt][1], c[nt][3]) > m[nt][1];
       }
-      if constexpr (S::kK8 != 0) {
+      if (__any_sync(~0u, grows)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint2 w = *reinterpret_cast<const uint2*>(sk + 2 * S::kK16 * 512 + (j * 32 + lane) * 8);
-          const uint32_t ws[2] = {w.x, w.y};
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t x = ws[s] ^ 0x80808080u;
-            if constexpr (S::kQRegs) {
-              mma_f16(c[j], qa[4 * S::kK16 + s], codes_lo(x), codes_hi(x));
-            } else {
-              uint32_t a[4];
-              load_q(S::kK16, s, a);
-              mma_f16(c[j], a, codes_lo(x), codes_hi(x));
-            }
-          }
-        }
-      }
-      // scores in powers of two, the block's value scale among them
-      const float f0 = qs0 * scale.x, f1 = qs1 * scale.x;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[j][0] = fmaf(c[j][0], f0, scale.y), c[j][1] = fmaf(c[j][1], f0, scale.y);
-        c[j][2] = fmaf(c[j][2], f1, scale.y), c[j][3] = fmaf(c[j][3], f1, scale.y);
-      }
-      const int token = (step0 + warp + kKaWarps * i) * kKaStep;
-      if (token + kKaStep > seen_by_all || scale.w == 0.0f) {  // (scale.w: there is no such block)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int nt = 0; nt < NT; ++nt) {
+          float a[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at_token = token + 8 * j + 2 * t + e;
-            if (at_token >= see0 || scale.w == 0.0f) c[j][e] = -INFINITY;
-            if (at_token >= see1 || scale.w == 0.0f) c[j][2 + e] = -INFINITY;
+            float x = fmaxf(c[nt][e], c[nt][2 + e]);
+#pragma unroll
+            for (int k = 4; k < 32; k *= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, k));
+            x = fmaxf(x, m[nt][e]);
+            a[e] = x == m[nt][e] ? 1.0f : exp2_fast(m[nt][e] - x);
+            m[nt][e] = x;
+            b[nt][e] = (x == -INFINITY ? 0.0f : x) - kKaLift;
+            l[nt][e] *= a[e];
           }
-      }
-      float x0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1]));
-      float x1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3]));
-      if (__any_sync(~0u, x0 > m0 || x1 > m1)) {
-        x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, 1)), x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, 1));
-        x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, 2)), x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, 2));
-        x0 = fmaxf(x0, m0), x1 = fmaxf(x1, m1);
-        const float a0 = x0 == m0 ? 1.0f : exp2_fast(m0 - x0), a1 = x1 == m1 ? 1.0f : exp2_fast(m1 - x1);
-        m0 = x0, m1 = x1;
-        b0 = (m0 == -INFINITY ? 0.0f : m0) - kKaLift, b1 = (m1 == -INFINITY ? 0.0f : m1) - kKaLift;
-        l0 *= a0, l1 *= a1;
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) o[k][0] *= a0, o[k][1] *= a0, o[k][2] *= a1, o[k][3] *= a1;
+          for (int k = 0; k < D / 16; ++k) o[k][nt][0] *= a[0], o[k][nt][1] *= a[1], o[k][nt][2] *= a[0], o[k][nt][3] *= a[1];
+        }
       }
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[j][0] = exp2_fast(c[j][0] - b0), c[j][1] = exp2_fast(c[j][1] - b0);
-        c[j][2] = exp2_fast(c[j][2] - b1), c[j][3] = exp2_fast(c[j][3] - b1);
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[nt][j] = exp2_fast(c[nt][j] - b[nt][j & 1]);
+        l[nt][0] = fmaf(c[nt][0] + c[nt][2], scale.vinv, l[nt][0]);
+        l[nt][1] = fmaf(c[nt][1] + c[nt][3], scale.vinv, l[nt][1]);
+        pb[nt][0] = transpose8(pack_half2(c[nt][0], c[nt][1]));
+        pb[nt][1] = transpose8(pack_half2(c[nt][2], c[nt][3]));
       }
-      l0 = fmaf((c[0][0] + c[0][1]) + (c[1][0] + c[1][1]), scale.z, l0);
-      l1 = fmaf((c[0][2] + c[0][3]) + (c[1][2] + c[1][3]), scale.z, l1);
-      const uint32_t pa[4] = {pack_half2(c[0][0], c[0][1]), pack_half2(c[0][2], c[0][3]), pack_half2(c[1][0], c[1][1]),
-                              pack_half2(c[1][2], c[1][3])};
-      // four columns' operands out of a word of each of four tokens
-      const uint8_t* sv = sk + S::kKBytes;
-      auto columns = [&](float (*acc)[4], uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {
+      // the operands of two MMAs, four d, out of a word of each of four tokens
+      auto values = [&](int tile, uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {
         const uint32_t x = __byte_perm(wa, wb, 0x5140) ^ 0x80808080u, y = __byte_perm(wc, wd, 0x5140) ^ 0x80808080u;
-        mma_f16(acc[0], pa, codes_lo(x), codes_lo(y));
-        mma_f16(acc[1], pa, codes_hi(x), codes_hi(y));
+        const uint32_t x0 = codes_lo(x), x1 = codes_hi(x), y0 = codes_lo(y), y1 = codes_hi(y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile][nt], x0, x1, y0, y1, pb[nt]);
         const uint32_t z = __byte_perm(wa, wb, 0x7362) ^ 0x80808080u, w = __byte_perm(wc, wd, 0x7362) ^ 0x80808080u;
-        mma_f16(acc[2], pa, codes_lo(z), codes_lo(w));
-        mma_f16(acc[3], pa, codes_hi(z), codes_hi(w));
+        const uint32_t z0 = codes_lo(z), z1 = codes_hi(z), w0 = codes_lo(w), w1 = codes_hi(w);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile + 1][nt], z0, z1, w0, w1, pb[nt]);
       };
 #pragma unroll
       for (int ch = 0; ch < S::kV16; ++ch) {
-        uint4 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(sv + ((u * S::kV16 + ch) * 32 + lane) * 16);
-        columns(o + 16 * ch, w[0].x, w[1].x, w[2].x, w[3].x);
-        columns(o + 16 * ch + 4, w[0].y, w[1].y, w[2].y, w[3].y);
-        columns(o + 16 * ch + 8, w[0].z, w[1].z, w[2].z, w[3].z);
-        columns(o + 16 * ch + 12, w[0].w, w[1].w, w[2].w, w[3].w);
+        values(8 * ch, v16[ch][0].x, v16[ch][1].x, v16[ch][2].x, v16[ch][3].x);
+        values(8 * ch + 2, v16[ch][0].y, v16[ch][1].y, v16[ch][2].y, v16[ch][3].y);
+        values(8 * ch + 4, v16[ch][0].z, v16[ch][1].z, v16[ch][2].z, v16[ch][3].z);
+        values(8 * ch + 6, v16[ch][0].w, v16[ch][1].w, v16[ch][2].w, v16[ch][3].w);
       }
       if constexpr (S::kV8 != 0) {
-        uint2 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint2*>(sv + 4 * S::kV16 * 512 + (u * 32 + lane) * 8);
-        columns(o + 16 * S::kV16, w[0].x, w[1].x, w[2].x, w[3].x);
-        columns(o + 16 * S::kV16 + 4, w[0].y, w[1].y, w[2].y, w[3].y);
+        values(8 * S::kV16, v8[0].x, v8[1].x, v8[2].x, v8[3].x);
+        values(8 * S::kV16 + 2, v8[0].y, v8[1].y, v8[2].y, v8[3].y);
       }
-      if constexpr (S::kV4 != 0) {
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[u] = *reinterpret_cast<const uint32_t*>(sv + 4 * S::kV16 * 512 + 4 * S::kV8 * 256 + (u * 32 + lane) * 4);
-        columns(o + 16 * S::kV16 + 8 * S::kV8, w[0], w[1], w[2], w[3]);
-      }
-      __syncwarp();  // scales[stage] has been read by all
-      issue(i + S::kStages - 1);
+      if constexpr (S::kV4 != 0) values(8 * S::kV16 + 4 * S::kV8, v4[0], v4[1], v4[2], v4[3]);
+      if (i + 1 < it.my_steps) load_values(off);
     }
-    cp_async_wait<0>();
+
+    // ---------------------------------------------------------- the next tile's first copies go ahead of this one's end
+    const KaItem done = it;
+    at = min(it.end, end);
+    const bool more = at < end;
+    if (more) begin_item();
 
     // ---------------------------------------------------------- the four warps' sums
-    l0 += __shfl_xor_sync(~0u, l0, 1), l1 += __shfl_xor_sync(~0u, l1, 1);
-    l0 += __shfl_xor_sync(~0u, l0, 2), l1 += __shfl_xor_sync(~0u, l1, 2);
-    if (t == 0) {
-      s_max[warp * kKaRows + g] = m0, s_max[warp * kKaRows + g + 8] = m1;
-      s_den[warp * kKaRows + g] = l0, s_den[warp * kKaRows + g + 8] = l1;
-    }
-    __syncthreads();
-    float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kKaWarps; ++w) top0 = fmaxf(top0, s_max[w * kKaRows + g]), top1 = fmaxf(top1, s_max[w * kKaRows + g + 8]);
-    const float a0 = m0 == top0 ? 1.0f : exp2_fast(m0 - top0), a1 = m1 == top1 ? 1.0f : exp2_fast(m1 - top1);
-    {
-      // columns: lane t of a wide chunk holds 32 successive ones, 16 in tile order from row 2 t, 16 from 2 t + 1
-      float* mine = reinterpret_cast<float*>(ring);
-      auto put = [&](int first_tile, int width, int d0) {
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], k);
+        if (g == 0) {
+          s_max[warp * ROWS + 8 * nt + 2 * t + e] = m[nt][e];
+          s_den[warp * ROWS + 8 * nt + 2 * t + e] = l[nt][e];
+        }
+      }
+    __syncthreads();
+    const bool whole = done.step0 == 0 && done.step1 == done.rq.steps;
+    const int which = done.step0 == 0 ? 1 : 0;
+    float* part_at = parts + (2 * (int64_t)blockIdx.x + which) * ka_part_floats(ROWS, D);
+    if (!whole && tid == 0) {
+      // The first CTA is the last one whose cut is not behind the tile's beginning, the last one is the last whose
+      // cut is before its end: see where cuts near a tile's ends go.
+      const int64_t start = done.end - done.rq.steps - kKaTileCost;
+      const int c0 = which ? (int)blockIdx.x : (int)ka_div(start + kKaTileCost + kKaMinPart - 1, share);
+      joins[which] = KaJoin{c0, (int)ka_div(done.end - kKaMinPart, share) - c0 + 1, done.rq.row0, done.h, done.tile, tile_rows, {0, 0}};
+    }
+    if (tid < ROWS) {
+      float top = -INFINITY, den = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * ROWS + tid]);
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) {
+        const float x = s_max[w * ROWS + tid];
+        den = fmaf(s_den[w * ROWS + tid], x == top ? 1.0f : exp2_fast(x - top), den);
+      }
+      s_inv[tid] = den == 0.0f ? 0.0f : 1.0f / den;  // a row that sees nothing is 0
+      if (!whole) part_at[tid] = top, part_at[ROWS + tid] = den;
+    }
+    float a[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * ROWS + 8 * nt + 2 * t + e]);
+        a[nt][e] = m[nt][e] == top ? 1.0f : exp2_fast(m[nt][e] - top);
+      }
+    // in turn: lane (g, t) holds `width` successive d of rows 2 t and 2 t + 1, two of each tile
+    auto put = [&](int first_tile, int width, int d0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < width; i += 4) {
-            const int col = d0 + width * (2 * t + e) + i;
-            *reinterpret_cast<float4*>(mine + g * S::kOPitch + col) =
-                make_float4(o[first_tile + i][e] * a0, o[first_tile + i + 1][e] * a0, o[first_tile + i + 2][e] * a0, o[first_tile + i + 3][e] * a0);
-            *reinterpret_cast<float4*>(mine + (g + 8) * S::kOPitch + col) =
-                make_float4(o[first_tile + i][2 + e] * a1, o[first_tile + i + 1][2 + e] * a1, o[first_tile + i + 2][2 + e] * a1,
-                            o[first_tile + i + 3][2 + e] * a1);
+            float4* to = reinterpret_cast<float4*>(s_o + (8 * nt + 2 * t + e) * S::kOPitch + d0 + width * g + i);
+            const float(&x)[4] = o[first_tile + i / 2][nt];
+            const float(&y)[4] = o[first_tile + i / 2 + 1][nt];
+            float4 v = warp == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *to;
+            v.x = fmaf(x[e], a[nt][e], v.x), v.y = fmaf(x[2 + e], a[nt][e], v.y);
+            v.z = fmaf(y[e], a[nt][e], v.z), v.w = fmaf(y[2 + e], a[nt][e], v.w);
+            *to = v;
           }
-      };
+    };
+    for (int w = 0; w < kKaWarps; ++w) {
+      if (warp == w) {
 #pragma unroll
-      for (int ch = 0; ch < S::kV16; ++ch) put(16 * ch, 16, 128 * ch);
-      if constexpr (S::kV8 != 0) put(16 * S::kV16, 8, 128 * S::kV16);
-      if constexpr (S::kV4 != 0) put(16 * S::kV16 + 8 * S::kV8, 4, 128 * S::kV16 + 64 * S::kV8);
-    }
-    __syncthreads();
-    const bool whole = step0 == 0 && step1 == rq.steps;
-    const int slot = 2 * (int)blockIdx.x + (first ? 0 : 1);
-    {
-      const int row = tid >> 3, part = tid & 7;
-      float top = -INFINITY, den = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * kKaRows + row]);
-#pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) {
-        const float m = s_max[w * kKaRows + row];
-        den += s_den[w * kKaRows + row] * (m == top ? 1.0f : exp2_fast(m - top));
+        for (int ch = 0; ch < S::kV16; ++ch) put(8 * ch, 16, 128 * ch);
+        if constexpr (S::kV8 != 0) put(8 * S::kV16, 8, 128 * S::kV16);
+        if constexpr (S::kV4 != 0) put(8 * S::kV16 + 4 * S::kV8, 4, 128 * S::kV16 + 64 * S::kV8);
       }
-      const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // a row that sees nothing is 0
-      const int64_t idx = (int64_t)tile * kKaRows + row, i = idx / p.group;
-      uint16_t* out = p.o + (rq.row0 + i) * p.ldo + ((int64_t)h * p.group + (idx - i * p.group)) * D;
-      float* part_at = parts + slot * ka_part_floats(D);
-      for (int col = 4 * part; col < D; col += 32) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kKaWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(ka_smem + w * S::kRing + (row * S::kOPitch + col) * 4);
-          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        if (!whole) {
-          *reinterpret_cast<float4*>(part_at + 2 * kKaRows + row * D + col) = v;
-        } else if (row < tile_rows) {
-          *reinterpret_cast<uint2*>(out + col) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-        }
+      __syncthreads();
+    }
+    for (int x = 4 * tid; x < ROWS * D; x += 4 * kKaThreads) {
+      const int row = x / D, col = x - row * D;
+      const float4 v = *reinterpret_cast<const float4*>(s_o + row * S::kOPitch + col);
+      if (!whole) {
+        *reinterpret_cast<float4*>(part_at + 2 * ROWS + x) = v;
+      } else if (row < tile_rows) {
+        const float inv = s_inv[row];
+        const int idx = done.tile * ROWS + row, i = idx / p.group;
+        *reinterpret_cast<uint2*>(p.o + (done.rq.row0 + i) * p.ldo + ((int64_t)done.h * p.group + (idx - i * p.group)) * D + col) =
+            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
       }
-      if (!whole && part == 0) part_at[row] = top, part_at[kKaRows + row] = den;
     }
-    if (step0 == 0 && step1 < rq.steps) {
-      join.parts = (int)((item_end - kKaMinPart) / share) - (int)blockIdx.x + 1;
-      join.slot = slot;
-      join.row0 = rq.row0;
-      join.head = h;
-      join.rows = tile_rows;
-      join.tile = tile;
-    }
-    first = false;
-    at += step1 - step0;
-    __syncthreads();  // the rings and the rows' sums have been read
+    if (!more) break;
+    __syncthreads();  // the rows' sums and scales have been read
   }
-  if (tid == 0) reinterpret_cast<KaJoin*>(p.ws)[blockIdx.x] = join;
 }
 
-// The parts of the tile that begins in CTA blockIdx.x of the launch before and goes on in the next ones, in
-// order: four rows to a CTA (blockIdx.y), a warp each.
-template <int D>
-__global__ void __launch_bounds__(128) k_kv_attn_join(KvAttnParams p) {
+// The parts of the tiles that several CTAs worked on.  CTA c of the launch before has one of each of its two; the rows
+// of a tile go round the CTAs that worked on it.  A row's parts are shared out over 1 to 16 warps, each
+// adds up its own in order, then the first one the others' sums.
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams p) {
+  constexpr int ROWS = 8 * NT;
+  __shared__ float s_sum[kKaJoinWarps][D];
+  __shared__ float s_top[kKaJoinWarps], s_den[kKaJoinWarps];
   grid_dependency_wait();
   grid_launch_dependents();
-  const KaJoin join = reinterpret_cast<const KaJoin*>(p.ws)[blockIdx.x];
-  const int lane = threadIdx.x & 31, row = 4 * blockIdx.y + (threadIdx.x >> 5);
-  if (join.parts == 0 || row >= join.rows) return;
-  const float* parts = p.ws + (int64_t)kKaMaxCtas * (sizeof(KaJoin) / 4);
-  // the first part is where it says, the others are the first ones of the CTAs that follow
-  auto at = [&](int k) { return parts + (int64_t)(k == 0 ? join.slot : 2 * ((int)blockIdx.x + k)) * ka_part_floats(D); };
-  float top = -INFINITY;
-  for (int k = lane; k < join.parts; k += 32) top = fmaxf(top, at(k)[row]);
+  const KaJoin* joins = reinterpret_cast<const KaJoin*>(p.ws) + 2 * blockIdx.x;
+  const KaJoin both[2] = {joins[0], joins[1]};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float* parts = p.ws + 2 * (int64_t)gridDim.x * (sizeof(KaJoin) / 4);
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
-  float v[D / 32], den = 0.0f;
+  for (int which = 0; which < 2; ++which) {
+    const KaJoin join = both[which];
+    if (join.parts == 0) continue;
+    auto at = [&](int k) { return parts + (2 * (int64_t)(join.first + k) + (k == 0 ? 1 : 0)) * ka_part_floats(ROWS, D); };
+    const int split = join.parts > 8 ? 16 : join.parts > 4 ? 8 : join.parts > 2 ? 4 : 2;  // warps to a row
+    const int at_once = kKaJoinWarps / split, mine = warp % split;
+    for (int row0 = (int)blockIdx.x - join.first; row0 < join.rows; row0 += at_once * join.parts) {
+      const int row = row0 + warp / split * join.parts;
+      float v[D / 32], den = 0.0f, top = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
+      for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
+      if (row < join.rows) {
 #pragma unroll 4
-  for (int k = 0; k < join.parts; ++k) {
-    const float* part = at(k);
-    const float m = part[row], a = m == top ? 1.0f : exp2_fast(m - top);
-    den = fmaf(part[kKaRows + row], a, den);
+        for (int k = mine; k < join.parts; k += split) {
+          const float* part = at(k);
+          const float x = part[row], y = part[ROWS + row];
+          float z[D / 32];
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) v[j] = fmaf(part[2 * kKaRows + row * D + 32 * j + lane], a, v[j]);
+          for (int j = 0; j < D / 32; ++j) z[j] = part[2 * ROWS + row * D + 32 * j + lane];
+          const float now = fmaxf(top, x), a = top == now ? 1.0f : exp2_fast(top - now), b = x == now ? 1.0f : exp2_fast(x - now);
+          den = fmaf(y, b, den * a);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) v[j] = fmaf(z[j], b, v[j] * a);
+          top = now;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) s_sum[warp][32 * j + lane] = v[j];
+      if (lane == 0) s_top[warp] = top, s_den[warp] = den;
+      __syncthreads();
+      if (mine == 0 && row < join.rows) {
+        float all = top;
+        for (int w = 1; w < split; ++w) all = fmaxf(all, s_top[warp + w]);
+        den = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
+        for (int w = 0; w < split; ++w) {
+          const float x = s_top[warp + w], a = x == all ? 1.0f : exp2_fast(x - all);
+          den = fmaf(s_den[warp + w], a, den);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) v[j] = fmaf(s_sum[warp + w][32 * j + lane], a, v[j]);
+        }
+        const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+        const int idx = join.tile * ROWS + row, i = idx / p.group;
+        uint16_t* out = p.o + (join.row0 + i) * p.ldo + ((int64_t)join.head * p.group + (idx - i * p.group)) * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) out[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] * inv));
+      }
+      __syncthreads();
+    }
   }
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t idx = (int64_t)join.tile * kKaRows + row, i = idx / p.group;
-  uint16_t* out = p.o + (join.row0 + i) * p.ldo + ((int64_t)join.head * p.group + (idx - i * p.group)) * D;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) out[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] * inv));
 }
 
 }  // namespace gbmlp

@@ -65,14 +65,14 @@ int launch_kv_write(const DeviceState* st, KvWriteParams& p, int d, cudaStream_t
   }
 }
 
-template <int D>
+template <int D, int NT>
 int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
-  auto kern = k_kv_attn<D>;
-  constexpr int smem = KaShape<D>::kBytes;
+  auto kern = k_kv_attn<D, NT>;
+  constexpr int smem = KaShape<D, NT>::kBytes;
   int ctas;
   {
     std::lock_guard<std::mutex> lock(g_setup_mu);
-    int& per_sm = st->kv_per_sm[D / 32 - 1];
+    int& per_sm = st->kv_per_sm[D / 32 - 1][NT - 1];
     if (per_sm == 0) {
       cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       int n = 0;
@@ -80,7 +80,7 @@ int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
       if (e != cudaSuccess || n < 1) return fail(MLP_ECUDA, "cache attention: %s", cudaGetErrorString(e));
       per_sm = n;
     }
-    ctas = per_sm * st->sms < kKaMaxCtas ? per_sm * st->sms : kKaMaxCtas;
+    ctas = std::min(per_sm * st->sms, ka_max_ctas(8 * NT, D));
   }
   int ts = trace_pre(s);
   cudaError_t e = launch_kernel(kern, dim3(ctas), dim3(kKaThreads), smem, s, 1, 1, p);
@@ -88,20 +88,31 @@ int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
   const int rc = launch_check(e, "cache attention");
   if (rc) return rc;
   ts = trace_pre(s);
-  e = launch_kernel(k_kv_attn_join<D>, dim3(ctas, kKaRows / 4), dim3(128), 0, s, 1, 1, p);
+  e = launch_kernel(k_kv_attn_join<D, NT>, dim3(ctas), dim3(32 * kKaJoinWarps), 0, s, 1, 1, p);
   trace_post(ts, s, kTraceKvJoin, ctas, D, 0);
   return launch_check(e, "cache attention, joining");
 }
 
+template <int D>
+int launch_kv_attn_d(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
+  // Tiles as high as a request's rows are on average: 8, 16 or, where the sums fit in registers, 24.
+  const int64_t rows = (p.rows + p.n - 1) / p.n * p.group;
+  if (rows <= 8) return launch_kv_attn_t<D, 1>(st, p, s);
+  if constexpr (D <= 128) {
+    if (rows > 16) return launch_kv_attn_t<D, 3>(st, p, s);
+  }
+  return launch_kv_attn_t<D, 2>(st, p, s);
+}
+
 int launch_kv_attn(DeviceState* st, const KvAttnParams& p, int d, cudaStream_t s) {
   switch (d / 32) {
-    case 1: return launch_kv_attn_t<32>(st, p, s);
-    case 2: return launch_kv_attn_t<64>(st, p, s);
-    case 3: return launch_kv_attn_t<96>(st, p, s);
-    case 4: return launch_kv_attn_t<128>(st, p, s);
-    case 5: return launch_kv_attn_t<160>(st, p, s);
-    case 6: return launch_kv_attn_t<192>(st, p, s);
-    case 7: return launch_kv_attn_t<224>(st, p, s);
-    default: return launch_kv_attn_t<256>(st, p, s);
+    case 1: return launch_kv_attn_d<32>(st, p, s);
+    case 2: return launch_kv_attn_d<64>(st, p, s);
+    case 3: return launch_kv_attn_d<96>(st, p, s);
+    case 4: return launch_kv_attn_d<128>(st, p, s);
+    case 5: return launch_kv_attn_d<160>(st, p, s);
+    case 6: return launch_kv_attn_d<192>(st, p, s);
+    case 7: return launch_kv_attn_d<224>(st, p, s);
+    default: return launch_kv_attn_d<256>(st, p, s);
   }
 }
