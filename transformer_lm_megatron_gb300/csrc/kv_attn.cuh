@@ -9,7 +9,7 @@
 //   - Work is counted in steps of 16 tokens, over all requests, heads and tiles of rows, and cut
 //     into equal shares, one for each CTA that fits on the GPU, wherever that falls: a long request
 //     spreads over all SMs, a ragged batch leaves none idle.  A tile that ends up with several
-//     CTAs leaves its parts (fp32 sums, maximum and denominator of each row) in the workspace, and
+//     CTAs leaves its parts (fp32 sums, base and denominator of each row) in the workspace, and
 //     k_kv_attn_join adds them up in order, so results do not change from run to run.
 //   - Each warp takes every fourth step of a share, alone: its lanes copy to shared memory,
 //     asynchronously and some steps ahead, the very bytes that they later feed to the tensor
@@ -24,9 +24,12 @@
 //     the codes are converted, and there are as few as 8 rows where tcgen05 wants 128 by 16 out of shared memory.
 //   - Queries go to fp16 with a power of two for each row that brings its largest element below
 //     2^15: exact but for elements under 2^-29 of it.
-//   - A block's value scale goes into the exponent: p' = exp2(s + log2(vscale) - max + 14) is the
-//     operand of the second product, at most 2^14, so that fp16 holds what is above 2^-28 of
-//     the largest in full precision, whatever the scales; the denominator adds p' / vscale in fp32.
+//   - A block's value scale goes into the exponent: p' = exp2(s + log2(vscale) - base) is the operand of the second
+//     product, whatever the scales; the denominator adds p' / vscale in fp32.  The base is the maximum of a row's
+//     first step less 10, and moves (and with it all sums so far) only where a p' would pass 2^15.5:
+//     with random scores the first step's is nearly always near enough, where a running maximum moves in
+//     half of a part's steps.  fp16 so holds a weight above 2^-24 of the largest in full precision, and below it
+//     to 2^-35 of the largest.
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -41,9 +44,11 @@ constexpr int kKaThreads = 32 * kKaWarps;
 constexpr int kKaStep = 16;        // tokens of a step
 constexpr int kKaWsRows = 19456;   // of the workspace, d + 2 floats each
 constexpr int kKaMinPart = 8;      // steps: no tile is cut nearer than this to either end
-constexpr int kKaTileCost = 8;     // steps that beginning and ending a tile takes as long as
-constexpr float kKaLift = 14.0f;   // p' is at most 2^14
-constexpr int kKaAhead = 4;        // steps of a warp, that many ahead asked for in L2
+constexpr int kKaTileCost = 16;    // steps that beginning and ending a tile takes as long as
+constexpr float kKaLift = 10.0f;   // a row's base is that far below its first maximum
+constexpr float kKaMost = 15.5f;   // p' is at most 2^15.5
+constexpr float kKaLowest = -3.0e38f;
+constexpr int kKaAhead = 2;        // steps of a warp, that many ahead asked for in L2
 constexpr int kKaJoinWarps = 16;
 
 struct KvAttnParams {
@@ -63,7 +68,7 @@ struct KvAttnParams {
   float* ws;
 };
 
-// The workspace: two descriptors for each CTA, then two parts (maxima, denominators, sums): of the tile that
+// The workspace: two descriptors for each CTA, then two parts (bases, denominators, sums): of the tile that
 // the CTA begins in the middle of, and of the one that it begins and another one goes on with.
 struct KaJoin {
   int first, parts, row0, head, tile, rows, pad[2];  // the CTA that began the tile; 0 parts: there is no such tile
@@ -141,8 +146,8 @@ struct KaShape {
   static constexpr int kOffPlace = 0;                                 // KaPlace of 64 steps of each warp
   static constexpr int kOffQ = kOffPlace + kKaWarps * 64 * 16;
   static constexpr int kOffO = kOffQ + kRows * kQPitch;
-  static constexpr int kOffRow = kOffO + kRows * kOPitch * 4;         // query scale of each row, then 1 / denominator
-  static constexpr int kOffMax = kOffRow + 2 * kRows * 4;             // [warps][rows] maxima, denominators
+  static constexpr int kOffRow = kOffO + kKaWarps * kRows * kOPitch * 4;  // query scale of each row
+  static constexpr int kOffMax = kOffRow + kRows * 4;                 // [warps][rows] bases, denominators
   static constexpr int kBytes = kOffMax + 2 * kKaWarps * kRows * 4;
 };
 
@@ -259,7 +264,6 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
 
   KaPlace* places = reinterpret_cast<KaPlace*>(ka_smem + S::kOffPlace) + warp * 64;
   float* s_qscale = reinterpret_cast<float*>(ka_smem + S::kOffRow);
-  float* s_inv = s_qscale + ROWS;
   float* s_max = reinterpret_cast<float*>(ka_smem + S::kOffMax);
   float* s_den = s_max + kKaWarps * ROWS;
   float* s_o = reinterpret_cast<float*>(ka_smem + S::kOffO);
@@ -284,38 +288,39 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
   };
 
   // ------------------------------------------------------------ reads
-  // lane l looks up the places of the warp's steps i0 + l; where those are a tile's first, it asks for the first
-  // few's codes as soon as it knows where they are
-  auto look_up = [&](int i0) {
+  // Lane l looks up the place of the warp's step i0 + l: `find` where the codes are, and asks for the block's
+  // scales (and, at a tile's beginning, for the first few steps' codes in L2); `settle` waits for them.
+  int found;
+  float most_k, most_v;
+  auto find = [&](int i0) {
     const int i = i0 + lane;
-    KaPlace pl = {~0, 0.0f, 0.0f, 0.0f};
+    found = ~0, most_k = most_v = 0.0f;
     if (i < it.my_steps) {
       const int token = (it.step0 + warp + kKaWarps * i) * kKaStep;
       const int b = token < it.rq.held ? p.table[(int64_t)it.r * p.width + (token >> p.log_bs)] : -1;
       if (b >= 0 && b < p.blocks) {
         const int64_t bh = (int64_t)b * p.nk + it.h;
-        pl.unit = (int)(bh << (p.log_bs - 4)) + ((token & ((1 << p.log_bs) - 1)) >> 4);
-        const float most = p.vmax[bh], kmost = p.kmax[bh];
+        found = (int)(bh << (p.log_bs - 4)) + ((token & ((1 << p.log_bs) - 1)) >> 4);
+        most_k = p.kmax[bh], most_v = p.vmax[bh];
         if (i < kKaAhead) {
-          prefetch_l2(p.kc + (int64_t)pl.unit * (16 * D), 16 * D);
-          prefetch_l2(p.vc + (int64_t)pl.unit * (16 * D), 16 * D);
+          prefetch_l2(p.kc + (int64_t)found * (16 * D), 16 * D);
+          prefetch_l2(p.vc + (int64_t)found * (16 * D), 16 * D);
         }
-        const float v = fmaxf(most * (1.0f / 127.0f), 7.703719777548943e-34f);  // at least 2^-110
-        const bool fine = most <= 3.4028234663852886e38f;
-        pl.kscale = kmost;
-        pl.vlog = fine ? log2f(v) : __uint_as_float(0x7FC00000u);
-        pl.vinv = fine ? __fdividef(1.0f, v) : 0.0f;
       }
     }
+  };
+  auto settle = [&](int i0) {
+    const float v = fmaxf(most_v * (1.0f / 127.0f), 7.703719777548943e-34f);  // at least 2^-110
+    const bool fine = most_v <= 3.4028234663852886e38f;
     __syncwarp();  // the places that these take the slots of have been read
-    places[i & 63] = pl;
+    places[(i0 + lane) & 63] = KaPlace{found, most_k, fine ? log2f(v) : __uint_as_float(0x7FC00000u), fine ? __fdividef(1.0f, v) : 0.0f};
     __syncwarp();
   };
   auto offset = [&](int unit) { return (int64_t)max(unit, ~unit) * (16 * D); };
   // asks for step i's codes in L2
   auto ahead = [&](int i) {
     if (i >= it.my_steps) return;
-    if ((i & 31) == 0) look_up(i);
+    if ((i & 31) == 0) find(i), settle(i);
     if (lane < 2) prefetch_l2((lane == 0 ? p.kc : p.vc) + offset(places[i & 63].unit), 16 * D);
   };
   uint4 k16[S::kK16 ? S::kK16 : 1][2], v16[S::kV16 ? S::kV16 : 1][4];
@@ -360,11 +365,12 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     next_item();
     load_queries();
     if (it.my_steps == 0) return;
-    look_up(0);
-    place = places[0];
-    off = offset(place.unit);
+    find(0);
+    off = offset(__shfl_sync(~0u, found, 0));
     load_keys(off);
     load_values(off);
+    settle(0);
+    place = places[0];
   };
   begin_item();
 
@@ -429,11 +435,11 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
-    float m[NT][2], b[NT][2], l[NT][2];  // maximum, what is taken off a score, denominator
+    float b[NT][2], l[NT][2];  // base, denominator
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, b[nt][e] = -kKaLift, l[nt][e] = 0.0f;
+      for (int e = 0; e < 2; ++e) b[nt][e] = kKaLowest, l[nt][e] = 0.0f;
 
     for (int i = 0; i < it.my_steps; ++i) {
       const KaPlace scale = place;
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
           for (int j = 0; j < 4; ++j)
             if (token + g + 8 * (j >> 1) >= see[nt][j & 1] || scale.unit < 0) c[nt][j] = -INFINITY;
         }
-        grows |= fmaxf(c[nt][0], c[nt][2]) > m[nt][0] || fmaxf(c[nt][1], c[nt][3]) > m[nt][1];
+        grows |= fmaxf(c[nt][0], c[nt][2]) - b[nt][0] > kKaMost || fmaxf(c[nt][1], c[nt][3]) - b[nt][1] > kKaMost;
       }
       if (__any_sync(~0u, grows)) {
 #pragma unroll
@@ -491,10 +497,9 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
             float x = fmaxf(c[nt][e], c[nt][2 + e]);
 #pragma unroll
             for (int k = 4; k < 32; k *= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, k));
-            x = fmaxf(x, m[nt][e]);
-            a[e] = x == m[nt][e] ? 1.0f : exp2_fast(m[nt][e] - x);
-            m[nt][e] = x;
-            b[nt][e] = (x == -INFINITY ? 0.0f : x) - kKaLift;
+            x = fmaxf(x - kKaLift, b[nt][e]);
+            a[e] = exp2_fast(b[nt][e] - x);
+            b[nt][e] = x;
             l[nt][e] *= a[e];
           }
 #pragma unroll
@@ -544,6 +549,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     if (more) begin_item();
 
     // ---------------------------------------------------------- the four warps' sums
+    // lane (g, t) holds `width` successive d of rows 2 t and 2 t + 1, two of each tile
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -551,10 +557,27 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
 #pragma unroll
         for (int k = 4; k < 32; k *= 2) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], k);
         if (g == 0) {
-          s_max[warp * ROWS + 8 * nt + 2 * t + e] = m[nt][e];
+          s_max[warp * ROWS + 8 * nt + 2 * t + e] = b[nt][e];
           s_den[warp * ROWS + 8 * nt + 2 * t + e] = l[nt][e];
         }
       }
+    auto put = [&](int first_tile, int width, int d0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < width; i += 4) {
+            const float(&x)[4] = o[first_tile + i / 2][nt];
+            const float(&y)[4] = o[first_tile + i / 2 + 1][nt];
+            *reinterpret_cast<float4*>(s_o + (warp * ROWS + 8 * nt + 2 * t + e) * S::kOPitch + d0 + width * g + i) =
+                make_float4(x[e], x[2 + e], y[e], y[2 + e]);
+          }
+    };
+#pragma unroll
+    for (int ch = 0; ch < S::kV16; ++ch) put(8 * ch, 16, 128 * ch);
+    if constexpr (S::kV8 != 0) put(8 * S::kV16, 8, 128 * S::kV16);
+    if constexpr (S::kV4 != 0) put(8 * S::kV16 + 4 * S::kV8, 4, 128 * S::kV16 + 64 * S::kV8);
     __syncthreads();
     const bool whole = done.step0 == 0 && done.step1 == done.rq.steps;
     const int which = done.step0 == 0 ? 1 : 0;
@@ -566,64 +589,36 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
       const int c0 = which ? (int)blockIdx.x : (int)ka_div(start + kKaTileCost + kKaMinPart - 1, share);
       joins[which] = KaJoin{c0, (int)ka_div(done.end - kKaMinPart, share) - c0 + 1, done.rq.row0, done.h, done.tile, tile_rows, {0, 0}};
     }
-    if (tid < ROWS) {
-      float top = -INFINITY, den = 0.0f;
+    // 16 lanes to a row
 #pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * ROWS + tid]);
+    for (int q = 0; q < NT; ++q) {
+      const int row = 8 * q + (tid >> 4), part = tid & 15;
+      float top = kKaLowest, den = 0.0f, a[kKaWarps];
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * ROWS + row]);
 #pragma unroll
       for (int w = 0; w < kKaWarps; ++w) {
-        const float x = s_max[w * ROWS + tid];
-        den = fmaf(s_den[w * ROWS + tid], x == top ? 1.0f : exp2_fast(x - top), den);
+        const float x = s_max[w * ROWS + row];
+        a[w] = exp2_fast(x - top);
+        den = fmaf(s_den[w * ROWS + row], a[w], den);
       }
-      s_inv[tid] = den == 0.0f ? 0.0f : 1.0f / den;  // a row that sees nothing is 0
-      if (!whole) part_at[tid] = top, part_at[ROWS + tid] = den;
-    }
-    float a[NT][2];
+      const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // a row that sees nothing is 0
+      if (!whole && part == 0) part_at[row] = top, part_at[ROWS + row] = den;
+      const int idx = done.tile * ROWS + row, i = idx / p.group;
+      uint16_t* out = p.o + (done.rq.row0 + i) * p.ldo + ((int64_t)done.h * p.group + (idx - i * p.group)) * D;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int col = 4 * part; col < D; col += 64) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kKaWarps; ++w) top = fmaxf(top, s_max[w * ROWS + 8 * nt + 2 * t + e]);
-        a[nt][e] = m[nt][e] == top ? 1.0f : exp2_fast(m[nt][e] - top);
-      }
-    // in turn: lane (g, t) holds `width` successive d of rows 2 t and 2 t + 1, two of each tile
-    auto put = [&](int first_tile, int width, int d0) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < width; i += 4) {
-            float4* to = reinterpret_cast<float4*>(s_o + (8 * nt + 2 * t + e) * S::kOPitch + d0 + width * g + i);
-            const float(&x)[4] = o[first_tile + i / 2][nt];
-            const float(&y)[4] = o[first_tile + i / 2 + 1][nt];
-            float4 v = warp == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *to;
-            v.x = fmaf(x[e], a[nt][e], v.x), v.y = fmaf(x[2 + e], a[nt][e], v.y);
-            v.z = fmaf(y[e], a[nt][e], v.z), v.w = fmaf(y[2 + e], a[nt][e], v.w);
-            *to = v;
-          }
-    };
-    for (int w = 0; w < kKaWarps; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int ch = 0; ch < S::kV16; ++ch) put(8 * ch, 16, 128 * ch);
-        if constexpr (S::kV8 != 0) put(8 * S::kV16, 8, 128 * S::kV16);
-        if constexpr (S::kV4 != 0) put(8 * S::kV16 + 4 * S::kV8, 4, 128 * S::kV16 + 64 * S::kV8);
-      }
-      __syncthreads();
-    }
-    for (int x = 4 * tid; x < ROWS * D; x += 4 * kKaThreads) {
-      const int row = x / D, col = x - row * D;
-      const float4 v = *reinterpret_cast<const float4*>(s_o + row * S::kOPitch + col);
-      if (!whole) {
-        *reinterpret_cast<float4*>(part_at + 2 * ROWS + x) = v;
-      } else if (row < tile_rows) {
-        const float inv = s_inv[row];
-        const int idx = done.tile * ROWS + row, i = idx / p.group;
-        *reinterpret_cast<uint2*>(p.o + (done.rq.row0 + i) * p.ldo + ((int64_t)done.h * p.group + (idx - i * p.group)) * D + col) =
-            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+        for (int w = 0; w < kKaWarps; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * S::kOPitch + col);
+          v.x = fmaf(x.x, a[w], v.x), v.y = fmaf(x.y, a[w], v.y), v.z = fmaf(x.z, a[w], v.z), v.w = fmaf(x.w, a[w], v.w);
+        }
+        if (!whole) {
+          *reinterpret_cast<float4*>(part_at + 2 * ROWS + row * D + col) = v;
+        } else if (row < tile_rows) {
+          *reinterpret_cast<uint2*>(out + col) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+        }
       }
     }
     if (!more) break;
@@ -654,7 +649,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams
     const int at_once = kKaJoinWarps / split, mine = warp % split;
     for (int row0 = (int)blockIdx.x - join.first; row0 < join.rows; row0 += at_once * join.parts) {
       const int row = row0 + warp / split * join.parts;
-      float v[D / 32], den = 0.0f, top = -INFINITY;
+      float v[D / 32], den = 0.0f, top = kKaLowest;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
       if (row < join.rows) {
@@ -665,7 +660,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams
           float z[D / 32];
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) z[j] = part[2 * ROWS + row * D + 32 * j + lane];
-          const float now = fmaxf(top, x), a = top == now ? 1.0f : exp2_fast(top - now), b = x == now ? 1.0f : exp2_fast(x - now);
+          const float now = fmaxf(top, x), a = exp2_fast(top - now), b = exp2_fast(x - now);
           den = fmaf(y, b, den * a);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) v[j] = fmaf(z[j], b, v[j] * a);
@@ -683,7 +678,7 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
         for (int w = 0; w < split; ++w) {
-          const float x = s_top[warp + w], a = x == all ? 1.0f : exp2_fast(x - all);
+          const float a = exp2_fast(s_top[warp + w] - all);
           den = fmaf(s_den[warp + w], a, den);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) v[j] = fmaf(s_sum[warp + w][32 * j + lane], a, v[j]);
