@@ -137,10 +137,11 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 template <int D, int NT>
 struct KaShape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtasPerSm = NT == 1 ? (D <= 128 ? 4 : D <= 192 ? 3 : 2) : NT == 2 && D <= 128 ? 3 : 2;
-  static constexpr bool kQRegs = NT * D <= 160;         // query operands in registers, else in shared memory
+  static constexpr int kCtasPerSm = NT == 1 ? (D <= 32 ? 4 : D <= 160 ? 3 : 2) : 2;
+  static constexpr bool kQRegs = NT * D <= 256;         // query operands in registers, else in shared memory
   static constexpr int kK16 = D / 64, kK8 = D / 32 % 2; // key chunks: 16 bytes a lane over 64 d, 8 over 32
   static constexpr int kV16 = D / 128, kV8 = D / 64 % 2, kV4 = D / 32 % 2;  // value chunks: 16, 8, 4 bytes a lane
+  static constexpr int kAtOnce = D <= 64 ? 2 : 1;       // steps that a warp works on at once
   static constexpr int kQPitch = 2 * D + 16;            // bytes of a query row
   static constexpr int kOPitch = D + 4;                 // floats of a row of sums
   static constexpr int kOffPlace = 0;                                 // KaPlace of 64 steps of each warp
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
   };
 
   // ------------------------------------------------------------ reads
+  constexpr int U = S::kAtOnce;
   // Lane l looks up the place of the warp's step i0 + l: `find` where the codes are, and asks for the block's
   // scales (and, at a tile's beginning, for the first few steps' codes in L2); `settle` waits for them.
   int found;
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
         const int64_t bh = (int64_t)b * p.nk + it.h;
         found = (int)(bh << (p.log_bs - 4)) + ((token & ((1 << p.log_bs) - 1)) >> 4);
         most_k = p.kmax[bh], most_v = p.vmax[bh];
-        if (i < kKaAhead) {
+        if (i < kKaAhead * U) {
           prefetch_l2(p.kc + (int64_t)found * (16 * D), 16 * D);
           prefetch_l2(p.vc + (int64_t)found * (16 * D), 16 * D);
         }
@@ -317,33 +319,41 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     __syncwarp();
   };
   auto offset = [&](int unit) { return (int64_t)max(unit, ~unit) * (16 * D); };
-  // asks for step i's codes in L2
+  // asks for the codes of steps i .. i + U - 1 in L2
   auto ahead = [&](int i) {
     if (i >= it.my_steps) return;
     if ((i & 31) == 0) find(i), settle(i);
-    if (lane < 2) prefetch_l2((lane == 0 ? p.kc : p.vc) + offset(places[i & 63].unit), 16 * D);
+    if (lane < 2 * U) prefetch_l2(((lane & 1) == 0 ? p.kc : p.vc) + offset(places[(i + (lane >> 1)) & 63].unit), 16 * D);
   };
-  uint4 k16[S::kK16 ? S::kK16 : 1][2], v16[S::kV16 ? S::kV16 : 1][4];
-  uint2 k8[2], v8[4];
-  uint32_t v4[4];
-  auto load_keys = [&](int64_t off) {
-    const int8_t* k = p.kc + off + g * D + 16 * t;
+  uint4 k16[U][S::kK16 ? S::kK16 : 1][2], v16[U][S::kV16 ? S::kV16 : 1][4];
+  uint2 k8[U][2], v8[U][4];
+  uint32_t v4[U][4];
+  KaPlace place[U];
+  int64_t off[U];
+  auto load_keys = [&]() {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int x = 0; x < U; ++x) {
+      const int8_t* k = p.kc + off[x] + g * D + 16 * t;
 #pragma unroll
-      for (int c = 0; c < S::kK16; ++c) k16[c][j] = ld_once16(k + j * 8 * D + 64 * c);
-      if constexpr (S::kK8 != 0) k8[j] = ld_once8(k + j * 8 * D + 64 * S::kK16 - 8 * t);
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int c = 0; c < S::kK16; ++c) k16[x][c][j] = ld_once16(k + j * 8 * D + 64 * c);
+        if constexpr (S::kK8 != 0) k8[x][j] = ld_once8(k + j * 8 * D + 64 * S::kK16 - 8 * t);
+      }
     }
   };
-  auto load_values = [&](int64_t off) {
-    const int8_t* v = p.vc + off + 2 * t * D;
+  auto load_values = [&]() {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int8_t* row = v + ((u & 1) + 8 * (u >> 1)) * D;
+    for (int x = 0; x < U; ++x) {
+      const int8_t* v = p.vc + off[x] + 2 * t * D;
 #pragma unroll
-      for (int c = 0; c < S::kV16; ++c) v16[c][u] = ld_once16(row + 128 * c + 16 * g);
-      if constexpr (S::kV8 != 0) v8[u] = ld_once8(row + 128 * S::kV16 + 8 * g);
-      if constexpr (S::kV4 != 0) v4[u] = ld_once4(row + 128 * S::kV16 + 64 * S::kV8 + 4 * g);
+      for (int u = 0; u < 4; ++u) {
+        const int8_t* row = v + ((u & 1) + 8 * (u >> 1)) * D;
+#pragma unroll
+        for (int c = 0; c < S::kV16; ++c) v16[x][c][u] = ld_once16(row + 128 * c + 16 * g);
+        if constexpr (S::kV8 != 0) v8[x][u] = ld_once8(row + 128 * S::kV16 + 8 * g);
+        if constexpr (S::kV4 != 0) v4[x][u] = ld_once4(row + 128 * S::kV16 + 64 * S::kV8 + 4 * g);
+      }
     }
   };
   // 16 lanes to a query row, 8 rows at a time (those behind the tile's last: zeros)
@@ -359,18 +369,18 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
       for (int j = 0; j < D / 32; ++j) qx[q][j] = there ? __ldg(src + 16 * j + (tid & 15)) : 0u;
     }
   };
-  KaPlace place;
-  int64_t off = 0;
   auto begin_item = [&]() {
     next_item();
     load_queries();
     if (it.my_steps == 0) return;
     find(0);
-    off = offset(__shfl_sync(~0u, found, 0));
-    load_keys(off);
-    load_values(off);
+#pragma unroll
+    for (int x = 0; x < U; ++x) off[x] = offset(__shfl_sync(~0u, found, x));
+    load_keys();
+    load_values();
     settle(0);
-    place = places[0];
+#pragma unroll
+    for (int x = 0; x < U; ++x) place[x] = places[x];
   };
   begin_item();
 
@@ -441,18 +451,25 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
 #pragma unroll
       for (int e = 0; e < 2; ++e) b[nt][e] = kKaLowest, l[nt][e] = 0.0f;
 
-    for (int i = 0; i < it.my_steps; ++i) {
-      const KaPlace scale = place;
-      ahead(i + kKaAhead);
-      if (i + 1 < it.my_steps) {
-        place = places[(i + 1) & 63];
-        off = offset(place.unit);
-      }
-      float c[NT][4];
+    for (int i = 0; i < it.my_steps; i += U) {
+      KaPlace scale[U];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
+      for (int x = 0; x < U; ++x) scale[x] = place[x];
+      ahead(i + kKaAhead * U);
+      if (i + U < it.my_steps) {
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          place[x] = places[(i + U + x) & 63];  // (behind the last step: a block that is not there)
+          off[x] = offset(place[x].unit);
+        }
+      }
+      float c[U][NT][4];
+#pragma unroll
+      for (int x = 0; x < U; ++x)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) c[x][nt][0] = c[x][nt][1] = c[x][nt][2] = c[x][nt][3] = 0.0f;
       // two k-steps: a word each of the keys of tokens g and g + 8
-      auto keys = [&](int chunk, int s, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+      auto keys = [&](float (&acc)[NT][4], int chunk, int s, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
         if constexpr (!S::kQRegs) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) load_q(chunk, s, nt, qb[0][nt], qb[1][nt]);
@@ -461,32 +478,42 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
         const uint32_t x = w0 ^ 0x80808080u, y = w1 ^ 0x80808080u, z = w2 ^ 0x80808080u, w = w3 ^ 0x80808080u;
         const uint32_t x0 = codes_lo(x), x1 = codes_hi(x), y0 = codes_lo(y), y1 = codes_hi(y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], x0, y0, x1, y1, qb[at_q][nt]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], x0, y0, x1, y1, qb[at_q][nt]);
         const uint32_t z0 = codes_lo(z), z1 = codes_hi(z), w0h = codes_lo(w), w1h = codes_hi(w);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], z0, w0h, z1, w1h, qb[at_q + 1][nt]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], z0, w0h, z1, w1h, qb[at_q + 1][nt]);
       };
 #pragma unroll
       for (int ch = 0; ch < S::kK16; ++ch) {
-        keys(ch, 0, k16[ch][0].x, k16[ch][1].x, k16[ch][0].y, k16[ch][1].y);
-        keys(ch, 2, k16[ch][0].z, k16[ch][1].z, k16[ch][0].w, k16[ch][1].w);
+#pragma unroll
+        for (int x = 0; x < U; ++x)
+          keys(c[x], ch, 0, k16[x][ch][0].x, k16[x][ch][1].x, k16[x][ch][0].y, k16[x][ch][1].y);
+#pragma unroll
+        for (int x = 0; x < U; ++x)
+          keys(c[x], ch, 2, k16[x][ch][0].z, k16[x][ch][1].z, k16[x][ch][0].w, k16[x][ch][1].w);
       }
-      if constexpr (S::kK8 != 0) keys(S::kK16, 0, k8[0].x, k8[1].x, k8[0].y, k8[1].y);
-      if (i + 1 < it.my_steps) load_keys(off);
+      if constexpr (S::kK8 != 0) {
+#pragma unroll
+        for (int x = 0; x < U; ++x) keys(c[x], S::kK16, 0, k8[x][0].x, k8[x][1].x, k8[x][0].y, k8[x][1].y);
+      }
+      if (i + U < it.my_steps) load_keys();
       // scores in powers of two, the block's value scale among them: token g + 8 (j / 2), row 2 t + j % 2
       bool grows = false;
-      const int token = (it.step0 + warp + kKaWarps * i) * kKaStep;
-      const bool masked = i >= first_masked || scale.unit < 0;  // (there is no such block)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int x = 0; x < U; ++x) {
+        const int token = (it.step0 + warp + kKaWarps * (i + x)) * kKaStep;
+        const bool masked = i + x >= first_masked || scale[x].unit < 0;  // (there is no such block)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[nt][j] = fmaf(c[nt][j], qs[nt][j & 1] * scale.kscale, scale.vlog);
-        if (masked) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (token + g + 8 * (j >> 1) >= see[nt][j & 1] || scale.unit < 0) c[nt][j] = -INFINITY;
+          for (int j = 0; j < 4; ++j) c[x][nt][j] = fmaf(c[x][nt][j], qs[nt][j & 1] * scale[x].kscale, scale[x].vlog);
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (token + g + 8 * (j >> 1) >= see[nt][j & 1] || scale[x].unit < 0) c[x][nt][j] = -INFINITY;
+          }
+          grows |= fmaxf(c[x][nt][0], c[x][nt][2]) - b[nt][0] > kKaMost || fmaxf(c[x][nt][1], c[x][nt][3]) - b[nt][1] > kKaMost;
         }
-        grows |= fmaxf(c[nt][0], c[nt][2]) - b[nt][0] > kKaMost || fmaxf(c[nt][1], c[nt][3]) - b[nt][1] > kKaMost;
       }
       if (__any_sync(~0u, grows)) {
 #pragma unroll
@@ -494,52 +521,62 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
           float a[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(c[nt][e], c[nt][2 + e]);
+            float top = fmaxf(c[0][nt][e], c[0][nt][2 + e]);
 #pragma unroll
-            for (int k = 4; k < 32; k *= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, k));
-            x = fmaxf(x - kKaLift, b[nt][e]);
-            a[e] = exp2_fast(b[nt][e] - x);
-            b[nt][e] = x;
+            for (int x = 1; x < U; ++x) top = fmaxf(top, fmaxf(c[x][nt][e], c[x][nt][2 + e]));
+#pragma unroll
+            for (int k = 4; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+            top = fmaxf(top - kKaLift, b[nt][e]);
+            a[e] = exp2_fast(b[nt][e] - top);
+            b[nt][e] = top;
             l[nt][e] *= a[e];
           }
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) o[k][nt][0] *= a[0], o[k][nt][1] *= a[1], o[k][nt][2] *= a[0], o[k][nt][3] *= a[1];
         }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[U][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int x = 0; x < U; ++x)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[nt][j] = exp2_fast(c[nt][j] - b[nt][j & 1]);
-        l[nt][0] = fmaf(c[nt][0] + c[nt][2], scale.vinv, l[nt][0]);
-        l[nt][1] = fmaf(c[nt][1] + c[nt][3], scale.vinv, l[nt][1]);
-        pb[nt][0] = transpose8(pack_half2(c[nt][0], c[nt][1]));
-        pb[nt][1] = transpose8(pack_half2(c[nt][2], c[nt][3]));
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+          float(&w)[4] = c[x][nt];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = exp2_fast(w[j] - b[nt][j & 1]);
+          l[nt][0] = fmaf(w[0] + w[2], scale[x].vinv, l[nt][0]);
+          l[nt][1] = fmaf(w[1] + w[3], scale[x].vinv, l[nt][1]);
+          pb[x][nt][0] = transpose8(pack_half2(w[0], w[1]));
+          pb[x][nt][1] = transpose8(pack_half2(w[2], w[3]));
+        }
       // the operands of two MMAs, four d, out of a word of each of four tokens
-      auto values = [&](int tile, uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {
+      auto values = [&](const uint32_t (&pw)[NT][2], int tile, uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {
         const uint32_t x = __byte_perm(wa, wb, 0x5140) ^ 0x80808080u, y = __byte_perm(wc, wd, 0x5140) ^ 0x80808080u;
         const uint32_t x0 = codes_lo(x), x1 = codes_hi(x), y0 = codes_lo(y), y1 = codes_hi(y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile][nt], x0, x1, y0, y1, pb[nt]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile][nt], x0, x1, y0, y1, pw[nt]);
         const uint32_t z = __byte_perm(wa, wb, 0x7362) ^ 0x80808080u, w = __byte_perm(wc, wd, 0x7362) ^ 0x80808080u;
         const uint32_t z0 = codes_lo(z), z1 = codes_hi(z), w0 = codes_lo(w), w1 = codes_hi(w);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile + 1][nt], z0, z1, w0, w1, pb[nt]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile + 1][nt], z0, z1, w0, w1, pw[nt]);
       };
 #pragma unroll
-      for (int ch = 0; ch < S::kV16; ++ch) {
-        values(8 * ch, v16[ch][0].x, v16[ch][1].x, v16[ch][2].x, v16[ch][3].x);
-        values(8 * ch + 2, v16[ch][0].y, v16[ch][1].y, v16[ch][2].y, v16[ch][3].y);
-        values(8 * ch + 4, v16[ch][0].z, v16[ch][1].z, v16[ch][2].z, v16[ch][3].z);
-        values(8 * ch + 6, v16[ch][0].w, v16[ch][1].w, v16[ch][2].w, v16[ch][3].w);
+      for (int x = 0; x < U; ++x) {
+#pragma unroll
+        for (int ch = 0; ch < S::kV16; ++ch) {
+          const uint4(&w)[4] = v16[x][ch];
+          values(pb[x], 8 * ch, w[0].x, w[1].x, w[2].x, w[3].x);
+          values(pb[x], 8 * ch + 2, w[0].y, w[1].y, w[2].y, w[3].y);
+          values(pb[x], 8 * ch + 4, w[0].z, w[1].z, w[2].z, w[3].z);
+          values(pb[x], 8 * ch + 6, w[0].w, w[1].w, w[2].w, w[3].w);
+        }
+        if constexpr (S::kV8 != 0) {
+          const uint2(&w)[4] = v8[x];
+          values(pb[x], 8 * S::kV16, w[0].x, w[1].x, w[2].x, w[3].x);
+          values(pb[x], 8 * S::kV16 + 2, w[0].y, w[1].y, w[2].y, w[3].y);
+        }
+        if constexpr (S::kV4 != 0) values(pb[x], 8 * S::kV16 + 4 * S::kV8, v4[x][0], v4[x][1], v4[x][2], v4[x][3]);
       }
-      if constexpr (S::kV8 != 0) {
-        values(8 * S::kV16, v8[0].x, v8[1].x, v8[2].x, v8[3].x);
-        values(8 * S::kV16 + 2, v8[0].y, v8[1].y, v8[2].y, v8[3].y);
-      }
-      if constexpr (S::kV4 != 0) values(8 * S::kV16 + 4 * S::kV8, v4[0], v4[1], v4[2], v4[3]);
-      if (i + 1 < it.my_steps) load_values(off);
+      if (i + U < it.my_steps) load_values();
     }
 
     // ---------------------------------------------------------- the next tile's first copies go ahead of this one's end
