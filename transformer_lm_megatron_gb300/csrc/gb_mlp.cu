@@ -1357,7 +1357,7 @@ int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* 
   DeviceState* st = nullptr;
   rc = device_state(&st);
   if (rc) return rc;
-  KvWriteParams p{tokens, {ldk, ldv}, nk, blocks, kv_log2(bs), 1, slots, {K, V}, {Kc, Vc}, {Kmax, Vmax}};
+  KvWriteParams p{tokens, {ldk, ldv}, nk, blocks, kv_log2(bs), 1, 1, slots, {K, V}, {Kc, Vc}, {Kmax, Vmax}};
   return launch_kv_write(st, p, d, static_cast<cudaStream_t>(stream));
 }
 

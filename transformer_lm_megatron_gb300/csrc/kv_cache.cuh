@@ -21,7 +21,7 @@ constexpr int kKvMaxHead = 256;
 constexpr int kKvMaxRequests = 4096;
 
 // ---------------------------------------------------------------- block tables and slots
-constexpr int kKvPlanThreads = 256;
+constexpr int kKvPlanThreads = 512;
 constexpr int kKvPlanRows = 1024;  // rows of a CTA
 
 enum KvPlanStatus : int { kKvNoBlocks = 1, kKvTableFull = 2, kKvNoRows = 4, kKvNegative = 8 };
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kKvPlanThreads) k_kv_plan(KvPlanParams p) {
 struct KvWriteParams {
   int64_t tokens, ld[2];  // rows' strides of K, V
   int nk, blocks, log_bs;
-  int chunk;              // tokens that a CTA looks through for the beginnings of its blocks: at most 32
+  int chunk;              // tokens among which a CTA looks for runs' beginnings: at most 64
+  int span;               // of the 2 nk heads of keys and values, those that a CTA takes
   const int* slots;
   const uint16_t* x[2];
   int8_t* codes[2];
@@ -161,95 +162,107 @@ __device__ __forceinline__ uint32_t kv_move4(uint32_t codes, float from, float t
   return kv_pack4(v[0], v[1], v[2], v[3]);
 }
 
-// One CTA of bs / 16 warps for each `chunk` tokens, head, and keys or values.  Tokens in slots next
+// One CTA of bs / 8 warps for each `chunk` tokens and `span` heads of keys or values.  Tokens in slots next
 // to each other in one block go together (a run, which begins where the token before is not in the slot
-// before): their rows are read once, into registers (16 tokens of a head to a warp, 16 bytes a
-// lane), their largest magnitude found, their codes written; the codes before them move
+// before): their rows are read once, into registers (16 bytes a
+// lane, always the same 8 elements of a head), their largest magnitude found, their codes written; the codes before them move
 // only where the maximum grows.  Every access is 16 or 8 bytes a lane and side by side, so the
 // copy rate bounds it over many tokens, and a launch with a chain of three loads over few.
-template <int D>
-__global__ void __launch_bounds__(128) k_kv_write(KvWriteParams p) {
-  constexpr int kPieces = D / 16;   // 16-byte pieces of 16 rows that a lane holds
-  constexpr int kRowPieces = D / 8; // of a row
-  __shared__ uint32_t s_most[2][4];
+template <int D, int BS>
+__global__ void __launch_bounds__(4 * BS) k_kv_write(KvWriteParams p) {
+  constexpr int kRowPieces = D / 8;                      // 16-byte pieces of a row
+  constexpr int kRows = 4 * BS / kRowPieces;             // rows at once
+  constexpr int kPieces = (BS + kRows - 1) / kRows;      // of a lane
+  __shared__ uint32_t s_most[2][BS / 8];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bs = 1 << p.log_bs;
-  int64_t rest = blockIdx.x;
-  const int h = (int)(rest % p.nk);
-  rest /= p.nk;
-  const int kv = (int)(rest & 1);
-  const int64_t t0 = (rest >> 1) * p.chunk;
-  const int64_t cap = (int64_t)p.blocks << p.log_bs;
-  const uint16_t* x = kv ? p.x[1] : p.x[0];
-  const int64_t ld = kv ? p.ld[1] : p.ld[0];
-  uint32_t leads;
-  {
-    const int64_t t = t0 + lane;
-    bool lead = false;
-    if (lane < p.chunk && t < p.tokens) {
-      const int s = p.slots[t], before = t > 0 ? p.slots[t - 1] : -2;
-      lead = s >= 0 && s < cap && ((s & (bs - 1)) == 0 || before != s - 1);
+  const unsigned spans = (2u * p.nk + p.span - 1) / p.span, rest = blockIdx.x / spans;
+  const int head0 = (int)(blockIdx.x - rest * spans) * p.span, head1 = min(head0 + p.span, 2 * p.nk);
+  const int64_t t0 = (int64_t)rest * p.chunk;
+  const int cap = p.blocks * BS;
+  const int row = (int)threadIdx.x / kRowPieces;
+  const int column = ((int)threadIdx.x - row * kRowPieces) * 8;
+  // of the chunk's tokens and a block's more: those that go on with a run, and of the chunk's: those that begin one
+  uint32_t goes_on[4] = {0, 0, 0, 0}, begins[2] = {0, 0};
+  int slots[2] = {-1, -1};
+#pragma unroll
+  for (int j = 0; j < BS / 16; ++j) {
+    const int64_t t = t0 + 32 * j + lane;
+    int s = -1, before = -2;
+    if (32 * j >= p.chunk + BS) break;
+    if (t < p.tokens) {
+      s = p.slots[t];
+      before = t > 0 ? p.slots[t - 1] : -2;
     }
-    leads = __ballot_sync(~0u, lead);
+    const bool there = s >= 0 && s < cap, on = there && (s & (BS - 1)) != 0 && before == s - 1;
+    goes_on[j] = __ballot_sync(~0u, on);
+    if (j < 2) {
+      begins[j] = __ballot_sync(~0u, there && !on && 32 * j + lane < p.chunk);
+      slots[j] = s;
+    }
   }
+  const uint64_t on_lo = goes_on[0] | (uint64_t)goes_on[1] << 32, on_hi = goes_on[2] | (uint64_t)goes_on[3] << 32;
+  uint64_t leads = begins[0] | (uint64_t)begins[1] << 32;
   int turn = 0;
   while (leads != 0) {
-    const int64_t t = t0 + __ffs(leads) - 1;
+    const int at_chunk = __ffsll((long long)leads) - 1;
     leads &= leads - 1;
-    const int slot = p.slots[t], off = slot & (bs - 1);
-    int count = 0;  // tokens of the run
-    for (int k = 0; k < bs - off; k += 32) {
-      const int64_t u = t + k + lane;
-      const uint32_t in = __ballot_sync(~0u, k + lane < bs - off && u < p.tokens && p.slots[u] == slot + k + lane);
-      count += in == ~0u ? 32 : __ffs(~in) - 1;
-      if (in != ~0u) break;
-    }
-    const int64_t bh = (int64_t)(slot >> p.log_bs) * p.nk + h;
-    float* most = (kv ? p.most[1] : p.most[0]) + bh;
-    int8_t* codes = (kv ? p.codes[1] : p.codes[0]) + (bh << p.log_bs) * D;
-    const float old = off > 0 ? *most : 0.0f;
-    uint4 v[kPieces];
-    __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+    const int64_t t = t0 + at_chunk;
+    const int slot = __shfl_sync(~0u, at_chunk < 32 ? slots[0] : slots[1], at_chunk & 31), off = slot & (BS - 1);
+    const uint64_t after = at_chunk == 63 ? on_hi : on_lo >> (at_chunk + 1) | on_hi << (63 - at_chunk);
+    const int count = ~after == 0 ? 65 : __ffsll((long long)~after);  // tokens of the run
+    const int last = row < kRows ? off + count : 0;  // (lanes that are left over have no rows)
+    for (int head = head0; head < head1; ++head) {
+      const int kv = head >= p.nk ? 1 : 0, h = kv ? head - p.nk : head;
+      const int64_t ld = kv ? p.ld[1] : p.ld[0];
+      const uint16_t* x = (kv ? p.x[1] : p.x[0]) + (int64_t)h * D + column;
+      const int64_t bh = (int64_t)(slot / BS) * p.nk + h;
+      float* most = (kv ? p.most[1] : p.most[0]) + bh;
+      int8_t* codes = (kv ? p.codes[1] : p.codes[0]) + (bh * BS + row) * D + column;
+      const float old = off > 0 ? *most : 0.0f;
+      uint4 v[kPieces];
+      __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+      const uint16_t* from = x + (t - off + row) * ld;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int i = lane + 32 * j, at = 16 * warp + i / kRowPieces;
-      v[j] = make_uint4(0, 0, 0, 0);
-      if (at >= off && at < off + count)
-        v[j] = *reinterpret_cast<const uint4*>(x + (t + at - off) * ld + (int64_t)h * D + (i % kRowPieces) * 8);
-    }
+      for (int j = 0; j < kPieces; ++j) {
+        const int at = row + j * kRows;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (at >= off && at < last) v[j] = *reinterpret_cast<const uint4*>(from);
+        from += kRows * ld;
+      }
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j)
-      for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
-        top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
-    // magnitudes in order of their bits, a NaN above all
-    uint32_t bits = (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
-    bits = __reduce_max_sync(~0u, bits);
-    if (bs > 16) {
+      for (int j = 0; j < kPieces; ++j)
+        for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
+          top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
+      // magnitudes in order of their bits, a NaN above all
+      uint32_t bits = (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
+      bits = __reduce_max_sync(~0u, bits);
       if (lane == 0) s_most[turn][warp] = bits;
       __syncthreads();
-      for (int w = 0; w < bs / 16; ++w) bits = max(bits, s_most[turn][w]);
+      for (int w = 0; w < BS / 8; ++w) bits = max(bits, s_most[turn][w]);
       turn ^= 1;
-    }
-    bits = max(bits, __float_as_uint(old) & 0x7FFFFFFFu);
-    const bool finite = bits < 0x7F800000u;
-    if (!finite) bits = 0x7FC00000u;  // a block with an infinity or a NaN reads as NaN
-    const float now = __uint_as_float(bits);
-    const float inv = finite && now >= kKvTiny ? __fdiv_ru(127.0f, now) : 0.0f;
-    const bool moves = off > 0 && finite && now != old;
+      bits = max(bits, __float_as_uint(old) & 0x7FFFFFFFu);
+      const bool finite = bits < 0x7F800000u;
+      if (!finite) bits = 0x7FC00000u;  // a block with an infinity or a NaN reads as NaN
+      const float now = __uint_as_float(bits);
+      const float inv = finite && now >= kKvTiny ? __fdiv_ru(127.0f, now) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int i = lane + 32 * j, at = 16 * warp + i / kRowPieces;
-      uint2* to = reinterpret_cast<uint2*>(codes + at * D + (i % kRowPieces) * 8);
-      if (at >= off && at < off + count) {
-        *to = finite ? make_uint2(kv_codes4(v[j].x, v[j].y, inv), kv_codes4(v[j].z, v[j].w, inv)) : make_uint2(0, 0);
-      } else if (at < off && moves) {
-        const uint2 c = *to;
-        *to = make_uint2(kv_move4(c.x, old, now), kv_move4(c.y, old, now));
+      for (int j = 0; j < kPieces; ++j) {
+        const int at = row + j * kRows;
+        if (at >= off && at < last)
+          *reinterpret_cast<uint2*>(codes + j * kRows * D) =
+              finite ? make_uint2(kv_codes4(v[j].x, v[j].y, inv), kv_codes4(v[j].z, v[j].w, inv)) : make_uint2(0, 0);
       }
+      if (off > 0 && finite && now != old && row < kRows) {
+        for (int at = row; at < off; at += kRows) {
+          uint2* to = reinterpret_cast<uint2*>(codes + (at - row) * D);
+          const uint2 c = *to;
+          *to = make_uint2(kv_move4(c.x, old, now), kv_move4(c.y, old, now));
+        }
+      }
+      if (threadIdx.x == 0) *most = now;
     }
-    if (threadIdx.x == 0) *most = now;
   }
 }
 

@@ -41,17 +41,22 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
 template <int D>
 int launch_kv_write_t(KvWriteParams& p, int64_t ctas, cudaStream_t s) {
   const int ts = trace_pre(s);
-  const cudaError_t e = launch_kernel(k_kv_write<D>, dim3((unsigned)ctas), dim3(2 << p.log_bs), 0, s, 1, 1, p);
+  auto kern = p.log_bs == 4 ? k_kv_write<D, 16> : p.log_bs == 5 ? k_kv_write<D, 32> : k_kv_write<D, 64>;
+  const cudaError_t e = launch_kernel(kern, dim3((unsigned)ctas), dim3(4 << p.log_bs), 0, s, 1, 1, p);
   trace_post(ts, s, kTraceKvWrite, p.tokens, 2 * (int64_t)p.nk * D, 0);
   return launch_check(e, "cache write");
 }
 
 int launch_kv_write(const DeviceState* st, KvWriteParams& p, int d, cudaStream_t s) {
-  // A CTA for each token gives a step's single tokens the most CTAs at once; a CTA for each
-  // 16 tokens spares prompts those that find no block beginning at their token.
-  const int64_t each = 2 * (int64_t)p.nk;
-  p.chunk = p.tokens * each <= (int64_t)st->sms * 64 ? 1 : 16;
-  const int64_t ctas = (p.tokens + p.chunk - 1) / p.chunk * each;
+  // A CTA for each token and head gives a step's single tokens the most CTAs at once.  Of more than two loads of CTAs,
+  // each takes up to a block's tokens, so that prompts have no CTAs that find no run beginning, and then several heads, which
+  // know where their tokens go.
+  const int64_t heads = 2 * (int64_t)p.nk, full = (int64_t)st->sms * (512 >> p.log_bs);
+  p.chunk = 1;
+  while (p.chunk < 1 << p.log_bs && p.tokens * heads >= full * p.chunk) p.chunk *= 2;
+  const int64_t chunks = (p.tokens + p.chunk - 1) / p.chunk;
+  p.span = (int)std::max<int64_t>(1, std::min<int64_t>(chunks * heads / full, 8));
+  const int64_t ctas = chunks * ((heads + p.span - 1) / p.span);
   if (ctas >= (int64_t)1 << 31) return fail(MLP_EUNSUPPORTED, "kv_write: %lld tokens of %d heads are too many for a launch", (long long)p.tokens, p.nk);
   switch (d / 32) {
     case 1: return launch_kv_write_t<32>(p, ctas, s);
