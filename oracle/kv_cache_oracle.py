@@ -34,7 +34,8 @@ def plan(add, lens, table, free, taken, bs, rows):
             table[r, b] = free[first[r] + b - have]
         for i in range(int(add[r])):
             p = old + i
-            pos[cu[r] + i], slots[cu[r] + i] = p, table[r, p // bs] * bs + p % bs
+            s = int(table[r, p // bs]) * bs + p % bs
+            pos[cu[r] + i], slots[cu[r] + i] = p, s if -(2**31) <= s < 2**31 else -1
     return 0, (lens + add).astype(np.int32), used, np.array(cu, np.int32), pos, slots, table
 
 

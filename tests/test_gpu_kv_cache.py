@@ -97,6 +97,17 @@ def test_plan_refuses_a_step_whole(change, bit):
     assert p.check() & bit
 
 
+def test_plan_with_entries_that_are_no_blocks():
+    """A partly filled block's entry that is no block gives a slot outside every pool, never one that wrapped round."""
+    p = Plan([3, 3, 3, 3], [1, 1, 1, 1], 2, 16, 9, 0, 12)
+    p.table[:, 0] = [2**31 - 1, -(2**31), 1 << 28, -1]
+    p.dev["table"] = i32(p.table)
+    p.run()
+    _status_ok()
+    assert p.check() == 0
+    assert bool((p.out["slots"] < 0).all())
+
+
 def test_plan_with_lengths_near_the_largest():
     """Sums that pass 32 bits are refused, not wrapped round."""
     p = Plan([2**31 - 1] * 5, [2**31 - 1] * 5, 8, 64, 100, 0, 70)

@@ -229,10 +229,17 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     }
     return all;
   };
-  for (int r0 = (p.n - 1) / kKaThreads * kKaThreads; r0 >= 0; r0 -= kKaThreads) {
-    total += group_sums(r0);
-    if (r0 > 0) __syncthreads();
+  if (p.n > kKaThreads) {
+    for (int r = kKaThreads + tid; r < p.n; r += kKaThreads) total += ka_request<ROWS>(p, r).weight(p.nk);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(~0u, total, k);
+    if (lane == 0) s_part[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int k = 0; k < kKaWarps; ++k) total += s_part[k];
+    __syncthreads();
   }
+  total += group_sums(0);
   const int64_t share = max(ka_div(total + gridDim.x - 1, gridDim.x), (int64_t)kKaMinPart);
   const int64_t raw[2] = {min(total, share * blockIdx.x), min(total, share * (blockIdx.x + 1))};
   if (tid == 0) s_cut[0] = raw[0], s_cut[1] = raw[1], s_first = p.n, s_begin = total;

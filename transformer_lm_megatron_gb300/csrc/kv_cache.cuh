@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kKvPlanThreads) k_kv_plan(KvPlanParams p) {
       int* cell = p.table + (int64_t)lo * p.width + b;
       const int block = b < have ? *cell : p.free[taken + s_first[lo] + b - have];
       if ((pos & (bs - 1)) == 0) *cell = block;  // a block that begins here is a new one
-      slot = (int)(((unsigned)block << p.log_bs) + (unsigned)(pos & (bs - 1)));
+      const int64_t wide = (int64_t)block * bs + (pos & (bs - 1));  // (what the table says need not be a block)
+      slot = wide == (int)wide ? (int)wide : -1;
     }
     p.pos[t] = pos;
     p.slots[t] = slot;

@@ -91,7 +91,8 @@ int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
   cudaError_t e = launch_kernel(kern, dim3(ctas), dim3(kKaThreads), smem, s, 1, 1, p);
   trace_post(ts, s, kTraceKvAttn, p.rows, (int64_t)p.nq * D, 0);
   const int rc = launch_check(e, "cache attention");
-  if (rc) return rc;
+  // (a table of fewer steps than two parts have: no tile is cut)
+  if (rc || (((int64_t)p.width << p.log_bs) + kKaStep - 1) / kKaStep < 2 * kKaMinPart) return rc;
   ts = trace_pre(s);
   e = launch_kernel(k_kv_attn_join<D, NT>, dim3(ctas), dim3(32 * kKaJoinWarps), 0, s, 1, 1, p);
   trace_post(ts, s, kTraceKvJoin, ctas, D, 0);
