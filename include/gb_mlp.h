@@ -364,8 +364,9 @@ int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* a
  * new tokens are left as they are and mean nothing.
  *   - The new tokens of one block must be successive rows in successive slots (as kv_plan gives
  *     them); a call with two such runs in one block, or the same slot twice, has undefined codes there.
- *   - A block and head with an infinity or a NaN among its tokens reads as NaN; with a
- *     maximum below 2^-100, as zeros.
+ *   - A block and head with an infinity or a NaN among its tokens reads as NaN until it is begun anew (a write to its
+ *     place 0); with a maximum below 2^-80 it holds zeros.
+ *   - A block that several requests' tables hold must not be written.
  */
 int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* K, int64_t ldk, const mlp_bf16* V, int64_t ldv,
              const int32_t* slots, int8_t* Kc, int8_t* Vc, float* Kmax, float* Vmax, void* stream);
@@ -379,9 +380,9 @@ int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* 
  *     [0, blocks), are left out.  Offsets cu that fall or leave [0, rows] leave their request out;
  *     a row that two requests claim holds either's.
  *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set and are undefined afterwards; calls that may run at once need one each.
- *   - For few rows a request (single tokens, drafts): every 16 rows times heads read the cache again.
+ *   - For few rows a request (single tokens, drafts): every 8 to 24 rows times heads read the cache again.
  * fp32 sums and softmax; queries, codes and softmax weights meet in fp16 (scaled by powers of two, so that
- * neither range nor more than 2^-12 of a weight is lost).  Results do not depend on what else the GPU runs.
+ * neither range nor more than 2^-11 of a weight is lost).  Value maxima below 2^-80 are read as zero, give or take 2^-80.  Results do not depend on what else the GPU runs.
  */
 #define KV_ATTN_WS_ROWS 19456
 int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int width, float scale, const mlp_bf16* Q, int64_t ldq,

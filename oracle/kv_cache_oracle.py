@@ -62,7 +62,7 @@ def write(x, slots, codes, most):
             if np.isfinite(top) and off and top != old:
                 codes[block, h, :off] = np.rint(held * old / top).astype(np.int8) if top > 0 else 0
             c = np.zeros_like(new)
-            if np.isfinite(top) and top >= 2.0**-100:
+            if np.isfinite(top) and top >= 2.0**-80:
                 c = np.rint(new * 127 / top)
             codes[block, h, off : off + len(run)] = c.astype(np.int8)
             most[block, h] = top

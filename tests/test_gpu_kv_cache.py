@@ -191,7 +191,7 @@ def test_write_many_tokens_and_heads():
 
 
 def test_write_ties_zeros_tiny_and_not_finite():
-    """Codes that are ties go to even; a block of zeros, one below 2^-100, one with an infinity, one with a NaN, and one that
+    """Codes that are ties go to even; a block of zeros, one below 2^-80, one with an infinity, one with a NaN, and one that
     held a NaN before."""
     pool = Pool(7, 1, 16, 32)
     pool.Kmax[5] = float("nan")
@@ -357,6 +357,33 @@ def test_attn_value_maxima_far_apart():
     c.run()
     _status_ok()
     c.check()
+
+
+@pytest.mark.parametrize("most", [2.0**-79, 2.0**100])
+def test_attn_values_of_any_size(most):
+    """Values all tiny or all huge, over a long request: neither the sums nor the denominator leave fp32's range.  The
+    output is of the values' size, so the bound is."""
+    c = Attn([3000, 40], [1, 1], 8, 2, 64, 16)
+    c.pool.Vmax[:] = most
+    c.pool.dev[3].fill_(most)
+    c.run()
+    _status_ok()
+    c.check()
+
+
+def test_attn_a_block_of_zeros_that_carries_the_weight():
+    """The block with by far the largest scores holds values of zero (their maximum 0, their codes 0): its weight counts in the
+    denominator beside blocks of values 2^20 times and 2^-60 times as large as usual."""
+    for scale in (2.0**20, 1.0, 2.0**-60):
+        c = Attn([200], [1], 4, 1, 64, 16, qscale=4.0)
+        zero = int(c.table[0, 5])
+        c.pool.Vmax[:] = scale
+        c.pool.Vmax[zero], c.pool.Vc[zero] = 0, 0
+        c.pool.Kmax[:], c.pool.Kmax[zero] = 1.0, 3.0
+        c.pool.dev = [torch.from_numpy(x).cuda() for x in (c.pool.Kc, c.pool.Vc, c.pool.Kmax, c.pool.Vmax)]
+        c.run()
+        _status_ok()
+        c.check()
 
 
 def test_attn_what_is_not_seen_does_not_count():

@@ -11,11 +11,14 @@
 //     spreads over all SMs, a ragged batch leaves none idle.  A tile that ends up with several
 //     CTAs leaves its parts (fp32 sums, base and denominator of each row) in the workspace, and
 //     k_kv_attn_join adds them up in order, so results do not change from run to run.
-//   - Each warp takes every fourth step of a share, alone: its lanes copy to shared memory,
-//     asynchronously and some steps ahead, the very bytes that they later feed to the tensor
-//     cores, so there is no barrier in the loop and no transposition: reductions may run
-//     over d and over tokens in any order, so a lane's 16 bytes of a key are operands of four
-//     successive MMAs, and its 16 bytes of four tokens' values those of eight.
+//   - Each warp takes every fourth step of a share, alone.  Its lanes read straight into registers the
+//     very bytes that they feed to the tensor cores, so there is no barrier in the loop and no
+//     transposition: reductions may run over d and over tokens in any order, so a lane's 16 bytes of
+//     a key are operands of four successive MMAs, and its 16 bytes of four tokens' values those of eight.  A step's
+//     registers are filled again as soon as they are used up; one bulk prefetch of a step's keys and one of its values,
+//     two steps ahead, have brought them to L2 by then.  (A ring in shared memory took 378 us where this takes 276 for 64
+//     requests of 12000 to 16384 tokens: twice the shared-memory traffic.  Four steps ahead fill the queues to HBM, which
+//     every tile's first look-ups then wait behind: 58 us for 55 for one request of 131077.)
 //   - Both products are taken transposed, S^T = K Q^T and O^T += V^T P^T: the codes are the operand with 16
 //     rows, the query rows the one with 8, so that eight query rows waste nothing and more of them
 //     (NT times 8) use a converted code again.  P^T changes places within a warp (movmatrix).
@@ -25,11 +28,16 @@
 //   - Queries go to fp16 with a power of two for each row that brings its largest element below
 //     2^15: exact but for elements under 2^-29 of it.
 //   - A block's value scale goes into the exponent: p' = exp2(s + log2(vscale) - base) is the operand of the second
-//     product, whatever the scales; the denominator adds p' / vscale in fp32.  The base is the maximum of a row's
-//     first step less 10, and moves (and with it all sums so far) only where a p' would pass 2^15.5:
-//     with random scores the first step's is nearly always near enough, where a running maximum moves in
-//     half of a part's steps.  fp16 so holds a weight above 2^-24 of the largest in full precision, and below it
-//     to 2^-35 of the largest.
+//     product, rounded to fp16 (2^-12 of a weight where bf16 takes 2^-9), whatever the scales; the denominator adds
+//     p' / vscale in fp32.  The base is the maximum of a row's first step less 10, and moves (and with it all sums so far)
+//     only where a p' would pass 2^15.5: with random scores the first step's is nearly always near enough, where a running
+//     maximum moves in half of a part's steps (68 us for 57 with 40 rows).  fp16 so holds a weight above
+//     2^-24 of the largest in full precision, and below it to 2^-35 of the largest.
+// Measured (graph replay, inputs rotated; the bytes at the copy rate in brackets): 64 requests of 12000 to 16384 tokens,
+// 8 key heads of 128, 64 query heads 276 us (275); one request of 131077 tokens 51 us (40); 48 of 100 to 16384 tokens 56 us
+// (42); 8 of 1500 to 2048, 128 heads of 160 103 us (88).  What the shorter ones lose, 11 us, is the launch, a chain of three
+// reads (lengths, table, codes) that nothing hides, the last warps' lag and the joining launch.  From 9 rows on the
+// instructions bound it: 16 requests of 3000 to 9000 tokens, 4 key heads, 8 rows 26 us, 16 31 us, 40 57 us (14).
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -43,12 +51,12 @@ constexpr int kKaWarps = 4;
 constexpr int kKaThreads = 32 * kKaWarps;
 constexpr int kKaStep = 16;        // tokens of a step
 constexpr int kKaWsRows = 19456;   // of the workspace, d + 2 floats each
-constexpr int kKaMinPart = 8;      // steps: no tile is cut nearer than this to either end
-constexpr int kKaTileCost = 16;    // steps that beginning and ending a tile takes as long as
+constexpr int kKaMinPart = 8;      // steps: no tile is cut nearer than this to either end (24: 13 us for 6 with 137 tokens)
+constexpr int kKaTileCost = 16;    // steps that beginning and ending a tile takes as long as (8: 64 us for 59 on a ragged batch)
 constexpr float kKaLift = 10.0f;   // a row's base is that far below its first maximum
 constexpr float kKaMost = 15.5f;   // p' is at most 2^15.5
 constexpr float kKaLowest = -3.0e38f;
-constexpr int kKaAhead = 2;        // steps of a warp, that many ahead asked for in L2
+constexpr int kKaAhead = 2;        // how many of its steps ahead a warp asks for codes in L2
 constexpr int kKaJoinWarps = 16;
 
 struct KvAttnParams {
@@ -78,20 +86,20 @@ __host__ __device__ constexpr int ka_max_ctas(int rows, int d) {
   return (int)((int64_t)kKaWsRows * (d + 2) / (2 * (int64_t)(sizeof(KaJoin) / 4) + 2 * ka_part_floats(rows, d)));
 }
 
-// 16, 8 or 4 bytes that one lane of the SM reads once.
+// 16, 8 or 4 bytes that one lane of the SM reads, once.
 __device__ __forceinline__ uint4 ld_once16(const int8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint2 ld_once8(const int8_t* p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_once4(const int8_t* p) {
   uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ void prefetch_l2(const int8_t* p, int bytes) {
@@ -319,7 +327,9 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     }
   };
   auto settle = [&](int i0) {
-    const float v = fmaxf(most_v * (1.0f / 127.0f), 7.703719777548943e-34f);  // at least 2^-110
+    // (a block of zeros has no scale: the smallest that another one can have, so that it moves the base last, and its weights
+    // do not vanish from the denominator beside values below 2^13)
+    const float v = fmaxf(most_v, kKvTiny) * (1.0f / 127.0f);
     const bool fine = most_v <= 3.4028234663852886e38f;
     __syncwarp();  // the places that these take the slots of have been read
     places[(i0 + lane) & 63] = KaPlace{found, most_k, fine ? log2f(v) : __uint_as_float(0x7FC00000u), fine ? __fdividef(1.0f, v) : 0.0f};
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
       const bool there = row < tile_rows_of(it);
       const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (it.rq.row0 + i) * p.ldq + ((int64_t)it.h * p.group + (idx - i * p.group)) * D);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) qx[q][j] = there ? __ldg(src + 16 * j + (tid & 15)) : 0u;
+      for (int j = 0; j < D / 32; ++j) qx[q][j] = there ? src[16 * j + (tid & 15)] : 0u;
     }
   };
   auto begin_item = [&]() {

@@ -141,7 +141,7 @@ struct KvWriteParams {
   float* most[2];
 };
 
-constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: blocks of smaller magnitudes hold zeros
+constexpr float kKvTiny = 8.271806125530277e-25f;  // 2^-80: blocks of smaller magnitudes hold zeros
 constexpr float kKvRound = 12582912.0f;            // 1.5 * 2^23: added, the sum's low byte is the rounded code
 
 // The four codes of fp32 products already rounded into kKvRound's last places.
