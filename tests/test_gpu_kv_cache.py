@@ -576,3 +576,57 @@ def test_two_captured_attentions_at_once():
         torch.cuda.synchronize()
         for c, w in zip(cases, want):
             assert torch.equal(c.O, w)
+
+
+@pytest.mark.parametrize("bs,nk,d", [(64, 64, 32), (32, 48, 96), (16, 40, 128), (64, 20, 160)])
+def test_write_many_heads(bs, nk, d):
+    """So many heads that a CTA takes a block's tokens and several heads: whole blocks, parts of them, runs of a few tokens and
+    single ones in any order, at any place of the CTA's tokens, over codes that move."""
+    rng = np.random.default_rng(bs + nk)
+    runs, block = [], 0
+    while sum(1 if r is None else r[2] for r in runs) < 420:
+        off = int(rng.integers(0, bs))
+        n = int(rng.choice([1, 1, 2, 5, bs]))
+        if n == bs:
+            off = int(rng.choice([0, off]))
+        runs.append((block, off, min(n, bs - off)))
+        block += 1
+        if rng.random() < 0.1:
+            runs.append(None)
+    order = rng.permutation(block)
+    runs = [r if r is None else (int(order[r[0]]), r[1], r[2]) for r in runs]
+    pool = Pool(block, nk, bs, d)
+    slots = _slots(runs, bs)
+    K, V = _rows(len(slots), nk, d, 16, 1), _rows(len(slots), nk, d, 0, 2, 2.0)
+    mlp.kv_write(K, V, i32(slots), *pool.dev)
+    _status_ok()
+    check_write(pool, K, V, slots)
+
+
+def test_calls_from_two_threads_on_two_streams():
+    """Each thread's writes and attention on a stream and a cache of its own give what they give alone."""
+    import threading
+
+    def work(seed, stream, out):
+        with torch.cuda.stream(stream):
+            c = Attn([700, 33], [1, 2], 8, 2, 96, 16, seed=seed)
+            slots = _slots([(0, 0, 16), (1, 0, 3)], 16)
+            K, V = _rows(19, 2, 96, 0, seed), _rows(19, 2, 96, 0, seed + 1)
+            for _ in range(20):
+                mlp.kv_write(K, V, i32(slots), *c.pool.dev)
+                c.run()
+            stream.synchronize()
+            out.append((c.O.clone(), [t.clone() for t in c.pool.dev]))
+
+    alone, both = [[], []], [[], []]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(2):
+        work(50 + 10 * k, streams[k], alone[k])
+    threads = [threading.Thread(target=work, args=(50 + 10 * k, streams[k], both[k])) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _status_ok()
+    for a, b in zip(alone, both):
+        assert torch.equal(a[0][0], b[0][0]) and all(torch.equal(x, y) for x, y in zip(a[0][1], b[0][1]))

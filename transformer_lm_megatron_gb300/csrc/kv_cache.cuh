@@ -204,7 +204,7 @@ __device__ __forceinline__ uint2 kv_codes8(uint4 x, const KvScale& s) {
 // requests 4.5 us, one for each of 4000 49 us (254 MB of codes move there; 73 us with a CTA to each).  A kernel for each
 // block size (rows and distances known) took 12.1 to 10.1 and 20.9 to 19.9 us.
 template <int D, int BS>
-__global__ void __launch_bounds__(4 * BS, BS == 64 && D <= 128 ? 5 : 1) k_kv_write(KvWriteParams p) {
+__global__ void __launch_bounds__(4 * BS, BS == 64 && D <= 128 ? 5 : 0) k_kv_write(KvWriteParams p) {
   constexpr int kRowPieces = D / 8;                      // 16-byte pieces of a row
   constexpr int kRows = 4 * BS / kRowPieces;             // rows at once
   constexpr int kPieces = (BS + kRows - 1) / kRows;      // of a lane
