@@ -379,10 +379,12 @@ int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* 
  *   - Tokens behind the table row's end (lens > width * bs), and those in a block whose entry is not in
  *     [0, blocks), are left out.  Offsets cu that fall or leave [0, rows] leave their request out;
  *     a row that two requests claim holds either's.
- *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set and are undefined afterwards; calls that may run at once need one each.
+ *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set
+ *     and are undefined afterwards; calls that may run at once need one each.
  *   - For few rows a request (single tokens, drafts): every 8 to 24 rows times heads read the cache again.
  * fp32 sums and softmax; queries, codes and softmax weights meet in fp16 (scaled by powers of two, so that
- * neither range nor more than 2^-11 of a weight is lost).  Value maxima below 2^-80 are read as zero, give or take 2^-80.  Results do not depend on what else the GPU runs.
+ * neither range nor more than 2^-11 of a weight is lost).  Value maxima below 2^-80 are read as zero, give or take
+ * 2^-80.  Results do not depend on what else the GPU runs.
  */
 #define KV_ATTN_WS_ROWS 19456
 int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int width, float scale, const mlp_bf16* Q, int64_t ldq,
