@@ -11,7 +11,6 @@
 // little above; everything else is at least 1/510 from a tie, far more than the rounding moves it.
 #pragma once
 #include <cstdint>
-#include <cuda_bf16.h>
 
 #include "ptx.cuh"
 
@@ -164,15 +163,14 @@ __device__ __forceinline__ uint32_t kv_move4(uint32_t codes, float from, float t
   return kv_pack4(v[0], v[1], v[2], v[3]);
 }
 
-// The largest magnitude of N pieces, as its bits: in the order of their bits, a NaN above all.
+// The largest magnitude of N pieces, as an fp32's bits: magnitudes are in the order of their bits, a NaN above all.
 template <int N>
 __device__ __forceinline__ uint32_t kv_top(const uint4 (&v)[N]) {
-  __nv_bfloat162 top = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+  uint32_t top = 0;  // of the low and of the high elements
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w})
-      top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162&>(w)));
-  return (uint32_t)max((int)(__bfloat16_as_ushort(top.x) & 0x7FFF), (int)(__bfloat16_as_ushort(top.y) & 0x7FFF)) << 16;
+    for (const uint32_t w : {v[j].x, v[j].y, v[j].z, v[j].w}) top = __vmaxu2(top, w & 0x7FFF7FFFu);
+  return max(top << 16, top & 0xFFFF0000u);
 }
 
 // A block's maximum with the new tokens' largest magnitude, and 127 / it.
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(4 * BS, BS == 64 && D <= 128 ? 5 : 0) k_kv_wri
       uint32_t bits = __reduce_max_sync(~0u, kv_top(v));
       if (lane == 0) s_most[turn][warp] = bits;
       __syncthreads();
-      for (int w = 0; w < BS / 8; ++w) bits = max(bits, s_most[turn][w]);
+      bits = __reduce_max_sync(~0u, s_most[turn][lane & (BS / 8 - 1)]);
       turn ^= 1;
       const KvScale sc = kv_scale(bits, old);
 #pragma unroll
