@@ -382,9 +382,9 @@ int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* 
  *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set
  *     and are undefined afterwards; calls that may run at once need one each.
  *   - For few rows a request (single tokens, drafts): every 8 to 24 rows times heads read the cache again.
- * fp32 sums and softmax; queries, codes and softmax weights meet in fp16 (scaled by powers of two, so that
- * neither range nor more than 2^-11 of a weight is lost).  Value maxima below 2^-80 are read as zero, give or take
- * 2^-80.  Results do not depend on what else the GPU runs.
+ * fp32 sums and softmax; queries, codes and softmax weights meet in fp16, scaled so that no range is lost: a weight times
+ * its block's value scale is off by at most 2^-11 of itself, or 2^-35 of the row's largest such product.  Value maxima
+ * below 2^-80 are read as zero, give or take 2^-80.  Results do not depend on what else the GPU runs.
  */
 #define KV_ATTN_WS_ROWS 19456
 int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int width, float scale, const mlp_bf16* Q, int64_t ldq,

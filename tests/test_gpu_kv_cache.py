@@ -7,7 +7,11 @@ Attention, a row's output o = sum p v with A = sum p |v| (p the softmax weights)
 bits are exact, at most 256 of them are added in fp32, the tensor cores' additions cut off instead of rounding),
 and by a few 2^-24 of the exponent's terms, at most 2^-15 of a weight while they stay below 2^6; each of the two counts for a weight and
 for the denominator, and o to half a bf16 step, 2^-8:
-    |got - o| <= A (2^-11 + 2 E 2^-19 + 2 2^-15) + 2^-8 |o|
+    |got - o| <= A (2^-11 + 2 E 2^-19 + 2 2^-15) + 2^-8 |o| + n 2^-35 M
+The last term: n tokens' weights times their scales, p' in the kernel, are fp16 too, whose smallest half step is 2^-25, and the base that
+they are taken from leaves the largest one of a row at 2^10 at least (the base moves to the largest less 10).  So the denominator,
+the sum of p' / scale, is at least 2^10 / max scale, and n products of 2^-25 with a code of at most 127 come to n 2^-35 of the
+largest value M that the request's blocks can hold, 127 times their largest scale.
 """
 import numpy as np
 import pytest
@@ -221,8 +225,14 @@ def test_write_leaves_out_slots_that_are_not_there():
 
 
 # ------------------------------------------------------------------------------------------ the attention
-def tolerance(o, A, E):
-    return A * (2.0**-11 + 2 * E[..., None] * 2.0**-19 + 2 * 2.0**-15) + 2.0**-8 * np.abs(o)
+def tolerance(o, A, E, n, M):
+    return A * (2.0**-11 + 2 * E[..., None] * 2.0**-19 + 2 * 2.0**-15) + 2.0**-8 * np.abs(o) + n * 2.0**-35 * M
+
+
+def largest(most, table, length, bs):
+    """The largest value that the blocks of a request's tokens can hold."""
+    blocks = [int(b) for b in table[: -(-max(length, 0) // bs)] if 0 <= b < len(most)]
+    return float(np.max(most[blocks])) if blocks else 0.0
 
 
 class Attn:
@@ -269,7 +279,8 @@ class Attn:
                 continue
             used[rows] = True
             o, A, E = kvo.attn(q[rows], p.Kc, p.Vc, p.Kmax, p.Vmax, self.table[r], int(self.lens[r]), scale)
-            right[rows] |= np.abs(got[rows] - o) <= tolerance(o, A, E)
+            length = min(int(self.lens[r]), self.width * self.bs)
+            right[rows] |= np.abs(got[rows] - o) <= tolerance(o, A, E, length, largest(p.Vmax, self.table[r], length, self.bs))
         wrong = np.argwhere(~right[used])
         assert len(wrong) == 0, (len(wrong), wrong[:5])
         w = self.whole.clone()
@@ -470,7 +481,7 @@ def test_cache_beyond_32_bit_offsets():
         np.testing.assert_array_equal(codes, want[0])
         np.testing.assert_array_equal(most.astype(np.float64), want[1])
     o, A, E = kvo.attn(to_f64(Q.cpu()), *held, table[0] - (blocks - 2), T, float(np.float32(d**-0.5)))
-    assert bool((np.abs(to_f64(O.cpu()) - o) <= tolerance(o, A, E)).all())
+    assert bool((np.abs(to_f64(O.cpu()) - o) <= tolerance(o, A, E, T, held[3].max())).all())
 
 
 # ------------------------------------------------------------------------------------------ a step of a serving loop
@@ -549,7 +560,7 @@ def test_serving_loop(captured):
         for r in range(n):
             at = slice(int(cu[r]), int(cu[r + 1]))
             o, A, E = kvo.attn(q[at], codes[0], codes[1], most[0], most[1], table[r], int(lens[r]), float(np.float32(d**-0.5)))
-            assert bool((np.abs(got[at] - o) <= tolerance(o, A, E)).all())
+            assert bool((np.abs(got[at] - o) <= tolerance(o, A, E, int(lens[r]), largest(most[1], table[r], int(lens[r]), bs))).all())
         assert bool((got[int(cu[n]) :] == 7).all())
 
 
@@ -630,3 +641,20 @@ def test_calls_from_two_threads_on_two_streams():
     _status_ok()
     for a, b in zip(alone, both):
         assert torch.equal(a[0][0], b[0][0]) and all(torch.equal(x, y) for x, y in zip(a[0][1], b[0][1]))
+
+
+@pytest.mark.parametrize("group,new", [(5, 1), (16, 1), (7, 3), (10, 4)])  # tiles of 8, 16 and 24 rows, one to three of them
+@pytest.mark.parametrize("d", range(32, 257, 32))
+def test_attn_every_head_size_and_tile(d, group, new):
+    """Requests over several CTAs and short ones, in every kernel that there is."""
+    c = Attn([1500, new, 90, 16], [new, new, new, new], 2 * group, 2, d, 16, pad=2, gap=8, seed=d + group)
+    c.run()
+    _status_ok()
+    c.check()
+
+
+def test_attn_as_many_requests_as_there_may_be():
+    c = Attn([3] * 4096, [1] * 4096, 1, 1, 32, 16, seed=2)
+    c.run()
+    _status_ok()
+    c.check()
