@@ -156,10 +156,13 @@ __device__ __forceinline__ uint32_t kv_codes4(uint32_t x01, uint32_t x23, float 
                   fmaf(bf16hi(x23), inv, kKvRound));
 }
 
+// round(code * from / to), from <= to.  `from` is taken 2^-8 times, so that no product leaves fp32 (127 times the largest bf16
+// would): exact, as it is 2^-80 at least where there are codes but 0, and the quotient's 2^8 come back with the rounding's sum.
 __device__ __forceinline__ uint32_t kv_move4(uint32_t codes, float from, float to) {
+  from *= 0.00390625f;
   float v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __fdiv_rn((float)(int8_t)(codes >> (8 * i)) * from, to) + kKvRound;
+  for (int i = 0; i < 4; ++i) v[i] = fmaf(__fdiv_rn((float)(int8_t)(codes >> (8 * i)) * from, to), 256.0f, kKvRound);
   return kv_pack4(v[0], v[1], v[2], v[3]);
 }
 
