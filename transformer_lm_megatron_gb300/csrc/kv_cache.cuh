@@ -3,12 +3,13 @@
 // Blocks of bs = 16, 32 or 64 tokens, a maximum for each block and head:
 //   Kc, Vc [blocks, nk, bs, d] int8, Kmax, Vmax [blocks, nk] fp32;  a code c stands for c * max / 127
 //
-// The maximum is kept, not max / 127: keys and values are bf16, so that products of a code
-// or of 127 with them are exact in fp32 and a division rounded once decides every rounding to
-// a code as exact arithmetic would.  New values are multiplied by 127 / max rounded up instead: of x * 127 /
-// max, quotients of 8-bit significands, a tie is either one where 127 divides max's (then 127 / max is a
-// power of two, the product exact) or +-63.5, at |x| = max / 2, which goes to the even 64 as it does from a
-// little above; everything else is at least 1/510 from a tie, far more than the rounding moves it.
+// The maximum is kept, not max / 127: keys and values are bf16, so that products of a code with a maximum are exact in
+// fp32 and a division rounded once decides every rounding to a code as exact arithmetic would.  New values are
+// multiplied by 127 / max rounded up instead.  With significands a of x and b of max, 8 bits each, and x's exponent t below max's,
+// x * 127 / max = 127 a / (b 2^t): a tie where 127 divides b (b = 254; 127 / max is then a power of two and the product
+// exact) or where |x| = max / 2 (+-63.5, which goes to the even 64 as it does from a little above).  Everything else is at least
+// 1 / (2 b 2^t) > 2^-(9 + t) from a tie, and the rounded factor moves the quotient, which is below 2^(8 - t), by less
+// than 2^-(15 + t).  The same holds for a moved code c old / new = c a / (b 2^t), whose one rounding moves it by half of that.
 #pragma once
 #include <cstdint>
 
