@@ -348,7 +348,7 @@ int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, ui
  *                          then the step is refused whole: the table stays as it was,
  *                          lens_out = lens, taken_out = taken, cu = 0, every slot -1.
  * Entries of the table and the free list are taken as they are: one that is no block gives slots that kv_write
- * leaves out.  The outputs must not lie over the inputs (a loop swaps two arrays of lengths).
+ * leaves out.  The outputs must not lie over the inputs (a loop swaps two arrays of lengths), the table, or one another.
  */
 int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* add, const int32_t* lens, int32_t* table,
             const int32_t* free_list, const int32_t* taken, int32_t* lens_out, int32_t* taken_out, int32_t* cu, int32_t* pos,

@@ -1332,6 +1332,10 @@ int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* a
     for (const auto& b : out)
       if (overlap(a.first, a.second, b.first, b.second))
         return fail(MLP_EINVAL, "%s: an output lies over an input (lens_out and taken_out are arrays of their own)", what);
+  for (const auto& a : out)
+    for (const auto& b : out)
+      if (&a != &b && overlap(a.first, a.second, b.first, b.second))
+        return fail(MLP_EINVAL, "%s: an output lies over the table or over another output", what);
   DeviceState* st = nullptr;
   rc = device_state(&st);
   if (rc) return rc;
