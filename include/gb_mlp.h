@@ -379,7 +379,7 @@ int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* 
  *   - Tokens behind the table row's end (lens > width * bs), and those in a block whose entry is not in
  *     [0, blocks), are left out.  Offsets cu that fall or leave [0, rows] leave their request out;
  *     a row that two requests claim holds either's.
- *   - O must not lie over Q.  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set
+ *   - O must not lie over Q (slices of the same buffer's rows may).  ws: KV_ATTN_WS_ROWS * (d + 2) floats of workspace, whose contents need not be set
  *     and are undefined afterwards; calls that may run at once need one each.
  *   - For few rows a request (single tokens, drafts): every 8 to 24 rows times heads read the cache again.
  * fp32 sums and softmax; queries, codes and softmax weights meet in fp16, scaled so that no range is lost: a weight times

@@ -20,6 +20,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 #include <string>
 #include <utility>
 
@@ -1381,7 +1382,7 @@ int kv_attn(int n, int64_t rows, int nq, int nk, int d, int bs, int blocks, int 
   if (!(scale > 0.0f && scale <= 3.0e38f)) return fail(MLP_EINVAL, "%s: scale = %g must be positive and finite", what, (double)scale);
   rc = check_qk_rows(what, "Q", Q, ldq, nq, d);
   if (!rc) rc = check_qk_rows(what, "O", O, ldo, nq, d);
-  if (!rc && Q == O) rc = fail(MLP_EINVAL, "%s: O must not lie over Q", what);
+  if (!rc && overlap_rows(Q, ldq, O, ldo, rows, (int64_t)nq * d)) rc = fail(MLP_EINVAL, "%s: O must not lie over Q", what);
   if (!rc) rc = check_ptrs("kv_attn (Kc, Vc, ws)", {Kc, Vc, ws});
   if (!rc) rc = check_kv_words(what, {{"Kmax", Kmax}, {"Vmax", Vmax}, {"table", table}, {"lens", lens}, {"cu", cu}});
   if (rc) return rc;

@@ -38,6 +38,16 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
+// Rows of `wide` 2-byte elements, lda and ldb apart, that may have elements in common.  (Slices of one buffer's rows do not:
+// their distance, less whole rows of it, leaves each the room that it takes.)
+bool overlap_rows(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t wide) {
+  if (!overlap(a, 2 * ((rows - 1) * lda + wide), b, 2 * ((rows - 1) * ldb + wide))) return false;
+  const int64_t pitch = std::gcd(lda, ldb);
+  int64_t apart = ((intptr_t)b - (intptr_t)a) / 2 % pitch;
+  if (apart < 0) apart += pitch;
+  return apart < wide || pitch - apart < wide;
+}
+
 template <int D>
 int launch_kv_write_t(KvWriteParams& p, int64_t ctas, cudaStream_t s) {
   const int ts = trace_pre(s);
