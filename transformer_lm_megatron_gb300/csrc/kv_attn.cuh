@@ -32,7 +32,7 @@
 //     p' / vscale in fp32.  The base is the maximum of a row's first step less 10, and moves (and with it all sums so far)
 //     only where a p' would pass 2^15.5: with random scores the first step's is nearly always near enough, where a running
 //     maximum moves in half of a part's steps (68 us for 57 with 40 rows).  fp16 so holds a weight above
-//     2^-24 of the largest in full precision, and below it to 2^-35 of the largest.
+//     2^-24 of the largest in full precision, and below it to 2^-35 of the largest.  Where scales lie 2^100 apart see kKaFar.
 // Measured (graph replay, inputs rotated; the bytes at the copy rate in brackets): 64 requests of 12000 to 16384 tokens,
 // 8 key heads of 128, 64 query heads 276 us (275); one request of 131077 tokens 51 us (40); 48 of 100 to 16384 tokens 56 us
 // (42); 8 of 1500 to 2048, 128 heads of 160 103 us (88).  What the shorter ones lose, 11 us, is the launch, a chain of three
@@ -56,6 +56,10 @@ constexpr int kKaTileCost = 16;    // steps that beginning and ending a tile tak
 constexpr float kKaLift = 10.0f;   // a row's base is that far below its first maximum
 constexpr float kKaMost = 15.5f;   // p' is at most 2^15.5
 constexpr float kKaLowest = -3.0e38f;
+// 2^-100: of weights whose block's scale is that far below the tile's largest (a block of zeros beside values above 2^20, say),
+// the denominator takes exp2(s - base) as the square of its root, which stays in fp32: p' may be 0 with weights that count.  Bases
+// may lie as far apart, so every factor between two of them is taken as a square too.
+constexpr float kKaFar = 7.888609052210118e-31f;
 constexpr int kKaAhead = 2;        // how many of its steps ahead a warp asks for codes in L2
 constexpr int kKaJoinWarps = 16;
 
@@ -156,6 +160,9 @@ struct KaShape {
   // Steps that a warp works on at once: what a step costs whatever its size counts for small heads (heads of 32 49 us for
   // 62, of 64 68 for 71), not for 128 (276 us either way, 102 us become 108 for 160).
   static constexpr int kAtOnce = D <= 64 ? 2 : 1;
+  // Each warp's largest value scale so far: in a register where there are more than 168 of them (40 rows 57.2 us for 59.2), else in
+  // shared memory (heads of 160 102.4 us for 105.6).
+  static constexpr bool kTopReg = NT > 1;
   static constexpr int kQPitch = 2 * D + 16;            // bytes of a query row
   static constexpr int kOPitch = D + 4;                 // floats of a row of sums
   static constexpr int kOffPlace = 0;                                 // KaPlace of 64 steps of each warp
@@ -163,11 +170,12 @@ struct KaShape {
   static constexpr int kOffO = kOffQ + kRows * kQPitch;
   static constexpr int kOffRow = kOffO + kKaWarps * kRows * kOPitch * 4;  // query scale of each row
   static constexpr int kOffMax = kOffRow + kRows * 4;                 // [warps][rows] bases, denominators
-  static constexpr int kBytes = kOffMax + 2 * kKaWarps * kRows * 4;
+  static constexpr int kOffTop = kOffMax + 2 * kKaWarps * kRows * 4;  // each warp's largest value scale in the tile so far
+  static constexpr int kBytes = kOffTop + kKaWarps * 4;
 };
 
 // Where a step's tokens are, in units of 16 tokens of a head from the pools' beginnings (complemented if their
-// block is not there: what it says is read all the same, and masked), and their scales.
+// block is not there: what it says is read all the same, and masked), and their scales.  vinv < 0: see kKaFar.
 struct __align__(16) KaPlace {
   int unit;
   float kscale, vlog, vinv;
@@ -289,6 +297,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
   float* s_max = reinterpret_cast<float*>(ka_smem + S::kOffMax);
   float* s_den = s_max + kKaWarps * ROWS;
   float* s_o = reinterpret_cast<float*>(ka_smem + S::kOffO);
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(ka_smem + S::kOffTop);
 
   // The tile that `at` is in (at < end, so there is one).
   KaItem it;
@@ -315,6 +324,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
   // scales (and, at a tile's beginning, for the first few steps' codes in L2); `settle` waits for them.
   int found;
   float most_k, most_v;
+  uint32_t top_so_far = 0;
   auto find = [&](int i0) {
     const int i = i0 + lane;
     found = ~0, most_k = most_v = 0.0f;
@@ -333,12 +343,18 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
     }
   };
   auto settle = [&](int i0) {
-    // (a block of zeros has no scale: the smallest that another one can have, so that it moves the base last, and its weights
-    // do not vanish from the denominator beside values below 2^13)
+    // (a block of zeros has no scale: the smallest that another one can have, so that it moves the base last)
     const float v = fmaxf(most_v, kKvTiny) * (1.0f / 127.0f);
     const bool fine = most_v <= 3.4028234663852886e38f;
-    __syncwarp();  // the places that these take the slots of have been read
-    places[(i0 + lane) & 63] = KaPlace{found, most_k, fine ? log2f(v) : __uint_as_float(0x7FC00000u), fine ? __fdividef(1.0f, v) : 0.0f};
+    // the largest scale that p' of these steps may meet in the base
+    uint32_t top = __reduce_max_sync(~0u, fine ? __float_as_uint(v) : 0u);
+    if (i0 > 0) top = max(top, S::kTopReg ? top_so_far : s_top[warp]);
+    top_so_far = top;
+    const bool far = v < __uint_as_float(top) * kKaFar;
+    __syncwarp();  // the places that these take the slots of, and s_top, have been read
+    places[(i0 + lane) & 63] =
+        KaPlace{found, most_k, fine ? log2f(v) : __uint_as_float(0x7FC00000u), !fine ? 0.0f : far ? -1.0f : __fdividef(1.0f, v)};
+    if (!S::kTopReg && lane == 0) s_top[warp] = top;
     __syncwarp();
   };
   auto offset = [&](int unit) { return (int64_t)max(unit, ~unit) * (16 * D); };
@@ -524,6 +540,7 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
       bool grows = false;
 #pragma unroll
       for (int x = 0; x < U; ++x) {
+        grows |= scale[x].vinv < 0.0f;
         const int token = (it.step0 + warp + kKaWarps * (i + x)) * kKaStep;
         const bool masked = i + x >= first_masked || scale[x].unit < 0;  // (there is no such block)
 #pragma unroll
@@ -550,12 +567,25 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
 #pragma unroll
             for (int k = 4; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
             top = fmaxf(top - kKaLift, b[nt][e]);
-            a[e] = exp2_fast(b[nt][e] - top);
+            const float half = exp2_fast(0.5f * (b[nt][e] - top));  // (see kKaFar)
+            a[e] = half * half;
+            l[nt][e] = l[nt][e] * half * half;
             b[nt][e] = top;
-            l[nt][e] *= a[e];
           }
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) o[k][nt][0] *= a[0], o[k][nt][1] *= a[1], o[k][nt][2] *= a[0], o[k][nt][3] *= a[1];
+        }
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          if (scale[x].vinv >= 0.0f) continue;
+          scale[x].vinv = 0.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float half = exp2_fast(0.5f * (c[x][nt][j] - b[nt][j & 1] - scale[x].vlog));
+              l[nt][j & 1] = fmaf(half, half, l[nt][j & 1]);
+            }
         }
       }
       uint32_t pb[U][NT][2];
@@ -659,8 +689,9 @@ __global__ void __launch_bounds__(kKaThreads, KaShape<D, NT>::kCtasPerSm) k_kv_a
 #pragma unroll
       for (int w = 0; w < kKaWarps; ++w) {
         const float x = s_max[w * ROWS + row];
-        a[w] = exp2_fast(x - top);
-        den = fmaf(s_den[w * ROWS + row], a[w], den);
+        const float half = exp2_fast(0.5f * (x - top));
+        a[w] = half * half;
+        den = fmaf(s_den[w * ROWS + row] * half, half, den);
       }
       const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // a row that sees nothing is 0
       if (!whole && part == 0) part_at[row] = top, part_at[ROWS + row] = den;
@@ -720,8 +751,9 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams
           float z[D / 32];
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) z[j] = part[2 * ROWS + row * D + 32 * j + lane];
-          const float now = fmaxf(top, x), a = exp2_fast(top - now), b = exp2_fast(x - now);
-          den = fmaf(y, b, den * a);
+          const float now = fmaxf(top, x), ah = exp2_fast(0.5f * (top - now)), bh = exp2_fast(0.5f * (x - now));
+          const float a = ah * ah, b = bh * bh;
+          den = fmaf(y * bh, bh, den * ah * ah);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) v[j] = fmaf(z[j], b, v[j] * a);
           top = now;
@@ -738,8 +770,8 @@ __global__ void __launch_bounds__(32 * kKaJoinWarps) k_kv_attn_join(KvAttnParams
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
         for (int w = 0; w < split; ++w) {
-          const float a = exp2_fast(s_top[warp + w] - all);
-          den = fmaf(s_den[warp + w], a, den);
+          const float half = exp2_fast(0.5f * (s_top[warp + w] - all)), a = half * half;
+          den = fmaf(s_den[warp + w] * half, half, den);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) v[j] = fmaf(s_sum[warp + w][32 * j + lane], a, v[j]);
         }
