@@ -2,13 +2,14 @@
 
 The rules are restated here, so that a case that no longer reaches its kernel fails.  Bounds are those of test_gpu_kv_cache.
 """
+import numpy as np
 import pytest
 import torch
 
 from transformer_lm_megatron_gb300 import build as gb_build
 from transformer_lm_megatron_gb300 import mlp
 
-from test_gpu_kv_cache import Attn, _rows, _status_ok
+from test_gpu_kv_cache import Attn, Pool, _rows, _slots, _status_ok, check_write, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,58 @@ def test_attn_a_block_size_of_every_kind_in_the_tile_of_eight_rows(d):
         c.run()
         _status_ok()
         c.check()
+
+
+def write_launch(tokens, nk, bs):
+    """(chunk, span) of kv_write: the tokens that a CTA looks through for runs, and the heads of keys and values that it takes."""
+    heads, full = 2 * nk, torch.cuda.get_device_properties(0).multi_processor_count * (512 // bs)
+    chunk = 1
+    while chunk < bs and tokens * heads >= full * chunk:
+        chunk *= 2
+    return chunk, max(1, min(-(-tokens // chunk) * heads // full, 8))
+
+
+# Key heads, so that a span begins with keys and ends with values, and the last one is not full.
+@pytest.mark.parametrize("bs,nk,d,tokens,span", [
+    (16, 45, 32, 3800, 4), (16, 131, 32, 2600, 8), (32, 65, 64, 2050, 3), (32, 49, 224, 2800, 3), (64, 33, 160, 2700, 2), (64, 131, 32, 2600, 8),
+    (16, 35, 128, 5000, 4), (64, 67, 96, 2000, 3)])
+def test_write_several_heads_a_cta(bs, nk, d, tokens, span):
+    """Whole blocks, parts of them, runs of a few tokens and single ones in any order, rows without a slot between them, over codes
+    that move."""
+    rng = np.random.default_rng(bs + nk)
+    runs, count = [], 0
+    while count < tokens:
+        off = int(rng.integers(0, bs))
+        n = int(rng.choice([1, 2, 7, bs, bs]))
+        if n == bs:
+            off = int(rng.choice([0, off]))
+        n = min(n, bs - off, tokens - count)
+        runs.append((len(runs), off, n))
+        count += n
+        if rng.random() < 0.1 and count < tokens:
+            runs.append(None)
+            count += 1
+    order = rng.permutation(len(runs))
+    runs = [r if r is None else (int(order[r[0]]), r[1], r[2]) for r in runs]
+    slots = _slots(runs, bs)
+    assert len(slots) == tokens and write_launch(tokens, nk, bs) == (bs, span)
+    assert nk % span != 0 and (2 * nk % span != 0 or span == 2)
+    pool = Pool(len(runs), nk, bs, d)
+    K, V = _rows(tokens, nk, d, 16, 1, 2.0), _rows(tokens, nk, d, 0, 2)
+    mlp.kv_write(K, V, i32(slots), *pool.dev)
+    _status_ok()
+    check_write(pool, K, V, slots)
+
+
+@pytest.mark.parametrize("bs,nk,tokens,chunk", [(16, 3, 5, 1), (64, 8, 600, 8), (32, 40, 2500, 32), (64, 3, 20000, 64)])
+def test_write_every_chunk(bs, nk, tokens, chunk):
+    """Prompts over whole blocks, one after another, for every number of tokens that a CTA looks through."""
+    assert write_launch(tokens, nk, bs)[0] == chunk
+    blocks = -(-tokens // bs) + 1
+    order = np.random.default_rng(nk).permutation(blocks)
+    slots = np.concatenate([b * bs + np.arange(bs) for b in order])[:tokens].astype(np.int32)
+    pool = Pool(blocks, nk, bs, 64)
+    K, V = _rows(tokens, nk, 64, 0, 1), _rows(tokens, nk, 64, 8, 2)
+    mlp.kv_write(K, V, i32(slots), *pool.dev)
+    _status_ok()
+    check_write(pool, K, V, slots)
