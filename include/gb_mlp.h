@@ -347,6 +347,9 @@ int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, ui
  *                          table row), 4 (more new tokens than rows), 8 (a negative length):
  *                          then the step is refused whole: the table stays as it was,
  *                          lens_out = lens, taken_out = taken, cu = 0, every slot -1.
+ * Tokens are taken back (drafts that were refused) and requests end by lowering lens between two steps.  Table entries at
+ * ceil(lens / bs) and behind are then no blocks of the request any more: a later step enters new ones over them.  So the
+ * caller gives each back first: taken -= 1, free_list[taken] = entry.
  * Entries of the table and the free list are taken as they are: one that is no block gives slots that kv_write
  * leaves out.  The outputs must not lie over the inputs (a loop swaps two arrays of lengths), the table, or one another.
  */
@@ -366,6 +369,8 @@ int kv_plan(int n, int bs, int width, int n_free, int64_t rows, const int32_t* a
  *     them); a call with two such runs in one block, or the same slot twice, has undefined codes there.
  *   - A block and head with an infinity or a NaN among its tokens reads as NaN until it is begun anew (a write to its
  *     place 0); with a maximum below 2^-80 it holds zeros.
+ *   - Tokens that a request took back (kv_plan) are held by its last block until that is begun anew: its maximum
+ *     stays what they raised it to, NaN if one of them was not finite.
  *   - A block that several requests' tables hold must not be written.
  */
 int kv_write(int64_t tokens, int nk, int d, int bs, int blocks, const mlp_bf16* K, int64_t ldk, const mlp_bf16* V, int64_t ldv,
