@@ -149,9 +149,11 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 template <int D, int NT>
 struct KaShape {
   static constexpr int kRows = 8 * NT;
-  // As many CTAs as need no spills: 64 long requests with heads of 128 take 276 us with 3, 287 us with 4 and spills; 16 query
-  // heads to a key head (32 requests of 4000 to 8000 tokens) 47 us with 2, 54 with 3 and spills; heads of 32 49 us with 4,
-  // 51 with 3; heads of 64 68 us with 3, 70 with 4.
+  // As many CTAs as leave a thread the registers that it needs: 64 long requests with heads of 128 take 276 us with 3, 287 us with 4
+  // and spills; 16 query heads to a key head (32 requests of 4000 to 8000 tokens) 47 us with 2, 54 with 3 and spills; heads of 32
+  // 49 us with 4, 51 with 3; heads of 64 68 us with 3, 70 with 4; heads of 192, 224 and 256 53, 62 and 67 us with 2, 57, 71 and
+  // 82 with 3 and spills.  Tiles of 16 rows of heads of 224 and 256 need more than the 255 that a thread can have (they spill 76 and 312
+  // bytes, with 1 CTA as with 2): 83 and 90 us with 16 query heads, where heads of 192 without spills take 67.
   static constexpr int kCtasPerSm = NT == 1 ? (D <= 32 ? 4 : D <= 160 ? 3 : 2) : 2;
   // Query operands in registers where they are 32 of them or fewer, else in shared memory (the 16 query heads: 47.3 us for 48.3).
   static constexpr bool kQRegs = NT * D <= 256;

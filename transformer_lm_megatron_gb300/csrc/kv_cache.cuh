@@ -205,6 +205,10 @@ __device__ __forceinline__ uint2 kv_codes8(uint4 x, const KvScale& s) {
 // heads of 128 10.8 us (6.4 of bytes), 753 tokens of 128 heads of 160 20.1 us (13.6), a token 2.0 us, one for each of 130
 // requests 4.5 us, one for each of 4000 49 us (254 MB of codes move there; 73 us with a CTA to each).  A kernel for each
 // block size (rows and distances known) took 12.1 to 10.1 and 20.9 to 19.9 us.
+// Of blocks of 64 tokens 5 CTAs of 8 warps are to fit, with 48 registers, for heads up to 128: 20,500 tokens of 1024 elements take
+// 38 us for 43 without that bound with heads of 64 (which then spill 28 bytes), 31 for 34 with 96, 28 for 30 with 128, 46 either
+// way with 32 (which spill too).  Other kernels are left the registers that they take, and spill up to 44 bytes: bound to 1024 threads an
+// SM, heads of 224 in blocks of 16 and 32 took 21 us for 22 and 23, smaller heads up to 1 us more, the rest 1 us less or the same.
 template <int D, int BS>
 __global__ void __launch_bounds__(4 * BS, BS == 64 && D <= 128 ? 5 : 0) k_kv_write(KvWriteParams p) {
   constexpr int kRowPieces = D / 8;                      // 16-byte pieces of a row
