@@ -111,7 +111,8 @@ int launch_kv_attn_t(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
 
 template <int D>
 int launch_kv_attn_d(DeviceState* st, const KvAttnParams& p, cudaStream_t s) {
-  // Tiles of 8, 16 or, where the sums fit in registers, 24 rows, for a request's rows on average.  A tile of 24 takes
+  // Tiles of 8, 16 or, where the sums fit in registers, 24 rows, for a request's rows on average, unused ones
+  // of the buffer among them (the header says what those cost).  A tile of 24 takes
   // 5/4 of the time of one of 16 (16 requests of 3000 to 9000 tokens: 17 us and 21 us a tile, 31 us a call with
   // 16 rows; with 40 rows 65 us in tiles of 16, 57 us in tiles of 24; with 32 48 us and 57 us).
   const int64_t rows = (p.rows + p.n - 1) / p.n * p.group;

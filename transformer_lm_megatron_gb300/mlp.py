@@ -440,7 +440,8 @@ def kv_attn_workspace(d: int) -> int:
 
 def kv_attn(Q, Kc, Vc, Kmax, Vmax, table, lens, cu, O, ws, scale=None, stream=None):
     """O = softmax(scale Q K^T) V of each request's rows cu[r] .. cu[r + 1] - 1 over its lens[r] cached tokens, the rows' own
-    the last of them.  Q, O [rows, nq, d] bf16, table [n, width], lens [n], cu [n + 1] int32; scale: 1 / sqrt(d) if None."""
+    the last of them.  Q, O [rows, nq, d] bf16, table [n, width], lens [n], cu [n + 1] int32; scale: 1 / sqrt(d) if None.
+    The launch is made for rows / n rows a request: of a larger buffer give the rows that the step can have (Q[:n], O[:n])."""
     dev = _device()
     (blocks, nk, bs, d), cache = _cache(Kc, Vc, Kmax, Vmax, dev)
     if Q is None or Q.dim() != 3 or table is None or table.dim() != 2:
