@@ -119,9 +119,9 @@ def test_write_every_chunk(bs, nk, tokens, chunk):
 
 @pytest.mark.parametrize("d,large", [(64, 3), (160, 2)])
 def test_attn_of_the_rows_that_there_are_and_of_a_whole_buffer(d, large):
-    """A buffer of 80 rows for 4 single tokens makes for larger tiles, its first 4 rows for those of one token."""
-    c = Attn([2000, 5, 0, 333], [1, 1, 1, 1], 16, 4, d, 32, pad=76)
-    assert tile(80, 4, 4, d) == large and tile(4, 4, 4, d) == 1
+    """A buffer of 72 rows for 4 single tokens makes for larger tiles, its first 4 rows for those of one token."""
+    c = Attn([2000, 5, 0, 333], [1, 1, 1, 1], 16, 4, d, 32, pad=68)
+    assert tile(72, 4, 4, d) == large and tile(4, 4, 4, d) == 1
     c.run()
     _status_ok()
     c.check()
