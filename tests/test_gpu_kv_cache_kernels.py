@@ -2,6 +2,10 @@
 
 The rules are restated here, so that a case that no longer reaches its kernel fails.  Bounds are those of test_gpu_kv_cache.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -129,3 +133,61 @@ def test_attn_of_the_rows_that_there_are_and_of_a_whole_buffer(d, large):
     mlp.kv_attn(c.Q[:4], *c.pool.dev, c.dt, c.dl, c.dc, c.O[:4], c.ws)
     _status_ok()
     c.check()
+
+
+@pytest.mark.parametrize("n", [127, 128, 129, 255, 256, 257, 384])
+@pytest.mark.parametrize("long", [128, 1000])
+def test_attn_requests_about_whole_groups(n, long):
+    """The work is counted in groups of 128 requests: equal ones, whose shares may end where a group does, the last of a group long."""
+    lens = [128] * n
+    lens[min(127, n - 1)] = lens[-1] = long
+    c = Attn(lens, [1] * n, 2, 1, 32, 16, seed=n)
+    c.run()
+    _status_ok()
+    c.check()
+
+
+FRESH = """
+import sys, threading
+sys.path[:0] = [".", "tests"]
+import torch
+import test_gpu_kv_cache as kv
+from transformer_lm_megatron_gb300 import mlp
+
+mlp.load()
+# heads and rows for a kernel of each kind: tiles of 8, 16 and 24 rows, and the write's block sizes
+CASES = [(64, 1, 1, 16), (96, 9, 1, 32), (128, 24, 1, 64), (160, 5, 1, 16), (256, 2, 6, 64)]
+
+
+def work(seed, stream, start):
+    with torch.cuda.stream(stream):
+        made = [(kv.Attn([700, 33], [new] * 2, 2 * group, 2, d, bs, seed=seed + d), kv._rows(19, 2, d, 0, seed)) for d, group, new, bs in CASES]
+        got = []
+        for c, K in made:
+            start()
+            mlp.kv_write(K, K, torch.arange(19, dtype=torch.int32, device="cuda"), *c.pool.dev)
+            start()
+            c.run()
+            got += [c.O, *c.pool.dev]
+        stream.synchronize()
+        return [t.clone() for t in got]
+
+
+streams = [torch.cuda.Stream() for _ in range(2)]
+barrier, outs = threading.Barrier(2, timeout=120), {}
+threads = [threading.Thread(target=lambda k=k: outs.__setitem__(k, work(k + 1, streams[k], barrier.wait))) for k in range(2)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+for k in range(2):
+    alone = work(k + 1, streams[k], lambda: None)
+    assert all(torch.equal(a, b) for a, b in zip(alone, outs[k])), k
+assert mlp.mlp_sync_status() == 0
+print("FIRST CALLS OK")
+"""
+
+
+def test_first_calls_from_two_threads():
+    """What a first launch works out is worked out once, whichever thread comes first."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "FIRST CALLS OK" in r.stdout, r.stdout + r.stderr
