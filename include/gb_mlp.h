@@ -331,7 +331,7 @@ int attn_rope_bwd(int h, int nh, int t, int64_t tokens, int seq_len, float p, ui
  *   Kmax, Vmax  [blocks, nk] fp32          the largest magnitude of a block's tokens for a head
  * where a code c stands for c * max / 127.  Request r's token j is at place j % bs of block
  * table[r][j / bs]; a token's slot is block * bs + place.  A step of a serving loop is
- *   kv_plan, (the layer's QKV projection), qk_norm_rope_fwd with kv_plan's positions, kv_write, kv_attn
+ *   kv_plan, (the caller's QKV projection), qk_norm_rope_fwd with kv_plan's positions, kv_write, kv_attn
  * with nothing read back by the host.  Tables, lengths and slots are device memory; what they hold is checked
  * where it is used, as said below.  Pointers to int32_t and float here need 4-byte alignment only, ws 16.
  *
